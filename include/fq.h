@@ -465,12 +465,105 @@ fq_status fq_moe_unpermute_reduce(const uint16_t *dxq_bf16, const int32_t *row_o
                                   const fq_act_q *aq, uint16_t *dx_bf16, float *dscale_a,
                                   void *ws, size_t ws_bytes, fq_stream stream);
 
+/* ------------------------------------------------------------------------
+ * fq_moe_tokens -- a whole MoE layer for a few tokens over the stored form of
+ * its weights (the real-quantized export above), as a decoding loop calls it:
+ * nothing is decoded to memory, permuted or gathered, and only the experts
+ * that the batch names are read (mcore_qad article, section 三: the formats'
+ * stored layouts are the deployment side's; QAT + ZeRO-3 page, convert).
+ *   h      = W_gu[e] . FQ_a1(x[t])                 [2F], gate first, fp32
+ *   A      = FQ_a2(silu(h[:F]) * h[F:])            bf16 when aq2 is NONE
+ *   out[t] = bf16(sum_j probs[t,j] * W_d[e_tj] . A)
+ *   over the slots j whose expert lies in [expert_begin, expert_begin +
+ *   E_local); a token without such a slot gets 0. A token may name an expert
+ *   twice (the weights add). Ids outside the range are not local.
+ *   W = value(code) * scale as fq_dequantize_stacked defines it, without its
+ *   rounding to bf16, except where the weight group is smaller than 64 (int8,
+ *   fp8) or not a multiple of 128 (int4) and not the whole row: then W is
+ *   the bf16 fake-quant value. Sums are fp32, in a fixed order (bitwise
+ *   reproducible).
+ * fq_stored_w: fmt FQ_FMT_*, group as in fq_weight_q (int4: the whole row or a
+ *   multiple of 32), codes [E, N, K] packed as exported (NONE: the raw bf16
+ *   stack, group and the scales unused); scale (int8, fp8, int4),
+ *   scale_bytes and global_scale (nvfp4), zero_point_bytes (int4).
+ *   w_gu is [E_local, 2F, H], w_d [E_local, H, F]; their formats may differ.
+ * x_bf16, out_bf16 [T, H]; expert_ids, probs [T, topk]. out must not overlap x.
+ * 0 <= T <= 128 (for more tokens the grouped GEMM calls are the path),
+ * 1 <= topk <= 64, E_local <= 1024, H and F % 16 == 0 and <= 16384.
+ * Workspace: fq_workspace_bytes(FQ_OP_MOE_TOKENS, {E_local, H, F}, T * topk,
+ * topk). Calls that may overlap on the device need workspaces of their own
+ * (two graphs captured over one workspace must not be replayed at once).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t fmt;
+  int32_t group;
+  const void *codes;
+  const float *scale;
+  const uint8_t *scale_bytes;
+  const uint8_t *zero_point_bytes;
+  const float *global_scale;
+} fq_stored_w;
+
+fq_status fq_moe_tokens(const uint16_t *x_bf16, int32_t T, int32_t H, int32_t F,
+                        const int32_t *expert_ids, const float *probs, int32_t topk,
+                        int32_t expert_begin, int32_t E_local, const fq_stored_w *w_gu,
+                        const fq_stored_w *w_d, const fq_act_q *aq1, const fq_act_q *aq2,
+                        uint16_t *out_bf16, void *ws, size_t ws_bytes, fq_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits: what the backward of a layer needs of its
+ * forward, kept as codes with fp32 scales instead of bf16 (the mcore_qad
+ * article, section 四, trains large models with full activation recompute;
+ * this is the cheaper half-way: nothing is recomputed by a GEMM).
+ *   fmt    FQ_FMT_INT8 or FQ_FMT_FP8_E4M3
+ *   group  elements per scale along a row: a power of two from 16 to 512 that
+ *          divides the row length K (fq_swiglu_*: that divides F)
+ *   codes  [rows, K], one byte per element (int8 two's complement, E4M3 byte)
+ *   scale  [rows, K/group] fp32
+ * Saved: amax of the group, s = max(amax * fp32(1/D), 2^-126) with D = 127
+ * (int8) or 448 (E4M3), s = 1 for an all-zero group; r = 1/s, code =
+ * Q(clamp(x * r)).
+ * Loaded: x~ = code * s. A group with an infinity or NaN stores s = NaN and
+ * codes 0: all of it loads as NaN. n_rows (device, NULL = all rows): only the
+ * first n_rows[0] rows are processed, the others of every output are left
+ * untouched.
+ *
+ * fq_ckpt_save: x [rows, K] bf16 -> codes, scale.
+ * fq_ckpt_load: codes, scale -> x [rows, K] bf16 = RNE(code * s).
+ * fq_swiglu_actfq_ckpt: fq_swiglu_actfq, bit for bit, that also saves h
+ *   (codes [R_max, 2F], scale [R_max, 2F/group]) in the same pass.
+ * fq_swiglu_bwd_ckpt: fq_swiglu_bwd from the saved h: with g, u the fp32
+ *   values code * s of the two halves, a~ = bf16(silu(g) * u), m_a its
+ *   activation-FQ mask, da = m_a * daq, dh and dS_a as there. aq_bf16 (or
+ *   NULL) receives FQ_a(a~) [R_max, F], the X operand of the down
+ *   projection's dScale, so that the forward's copy need not be kept.
+ *   dscale_a, ws, ws_bytes as for fq_swiglu_bwd.
+ * K, F % 16 == 0; rows * K and R_max * 2F < 2^34; bf16 tensors and codes
+ * 16-byte aligned, scale 4-byte aligned. In-place use (an output overlapping
+ * an input) is not supported.
+ * ---------------------------------------------------------------------- */
+fq_status fq_ckpt_save(const uint16_t *x_bf16, int32_t rows, int32_t K, const int32_t *n_rows,
+                       int32_t fmt, int32_t group, uint8_t *codes, float *scale, fq_stream stream);
+fq_status fq_ckpt_load(const uint8_t *codes, const float *scale, int32_t rows, int32_t K,
+                       const int32_t *n_rows, int32_t fmt, int32_t group, uint16_t *x_bf16,
+                       fq_stream stream);
+fq_status fq_swiglu_actfq_ckpt(const uint16_t *h_bf16, int32_t R_max, const int32_t *n_rows,
+                               int32_t F, const fq_act_q *aq, int32_t fmt, int32_t group,
+                               uint16_t *a_bf16, uint16_t *aq_bf16, uint8_t *codes, float *scale,
+                               fq_stream stream);
+fq_status fq_swiglu_bwd_ckpt(const uint16_t *daq_bf16, const uint8_t *codes, const float *scale,
+                             int32_t R_max, const int32_t *n_rows, int32_t F, int32_t fmt,
+                             int32_t group, const fq_act_q *aq, uint16_t *dh_bf16,
+                             uint16_t *aq_bf16, float *dscale_a, void *ws, size_t ws_bytes,
+                             fq_stream stream);
+
 /* Workspace sizing. op: one of FQ_OP_*. fmts = weight fmt | act fmt << 8. */
 #define FQ_OP_PERMUTE 1
 #define FQ_OP_GEMM_FWD 2
 #define FQ_OP_GEMM_BWD 3
 #define FQ_OP_ACT_SCALE_GRAD 4 /* shape = {1, rows, cols}; R_max, fmts unused */
 #define FQ_OP_TOPK_KL 5        /* shape, R_max, fmts unused */
+#define FQ_OP_MOE_TOKENS 6     /* shape = {E_local, H, F}, R_max = T * topk, fmts = topk */
 size_t fq_workspace_bytes(int32_t op, fq_shape shape, int32_t R_max, int32_t fmts);
 
 const char *fq_last_error(void);

@@ -39,6 +39,7 @@ FQ_OP_GEMM_FWD = 2
 FQ_OP_GEMM_BWD = 3
 FQ_OP_ACT_SCALE_GRAD = 4
 FQ_OP_TOPK_KL = 5
+FQ_OP_MOE_TOKENS = 6
 FQ_GROUP_TENSOR = -1     # one weight scale per expert matrix (int8 / fp8)
 
 EXPORTED = (
@@ -47,7 +48,8 @@ EXPORTED = (
     "fq_moe_combine", "fq_moe_combine_bwd", "fq_moe_unpermute_reduce", "fq_workspace_bytes",
     "fq_last_error", "fq_abi_version", "fq_export_scales", "fq_dequantize_stacked", "fq_topk_kl",
     "fq_moe_permute_noalloc", "fq_validate", "fq_actfq", "fq_grouped_gemm_fwd_tokens",
-    "fq_grouped_gemm_wgrad_tokens",
+    "fq_grouped_gemm_wgrad_tokens", "fq_ckpt_save", "fq_ckpt_load", "fq_swiglu_actfq_ckpt",
+    "fq_swiglu_bwd_ckpt", "fq_moe_tokens",
 )
 
 FQ_BAD_EXPERT_ID = 0x01
@@ -77,6 +79,12 @@ class fq_weight_q(ctypes.Structure):
 
 class fq_act_q(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int32), ("scale", ctypes.c_void_p)]
+
+
+class fq_stored_w(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("group", ctypes.c_int32), ("codes", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("scale_bytes", ctypes.c_void_p),
+                ("zero_point_bytes", ctypes.c_void_p), ("global_scale", ctypes.c_void_p)]
 
 
 def _load() -> ctypes.CDLL:
@@ -113,6 +121,15 @@ def _load() -> ctypes.CDLL:
         "fq_export_scales": (st, [fq_shape, ctypes.POINTER(fq_weight_q), P, P, P]),
         "fq_dequantize_stacked": (st, [P, fq_shape, I32, I32, P, P, P, P, P, P]),
         "fq_topk_kl": (st, [P, P, I32, I32, I32, I32, P, P, P, P, P, P, SZ, P]),
+        "fq_moe_tokens": (st, [P, I32, I32, I32, P, P, I32, I32, I32, ctypes.POINTER(fq_stored_w),
+                               ctypes.POINTER(fq_stored_w), ctypes.POINTER(fq_act_q),
+                               ctypes.POINTER(fq_act_q), P, P, SZ, P]),
+        "fq_ckpt_save": (st, [P, I32, I32, P, I32, I32, P, P, P]),
+        "fq_ckpt_load": (st, [P, P, I32, I32, P, I32, I32, P, P]),
+        "fq_swiglu_actfq_ckpt": (st, [P, I32, P, I32, ctypes.POINTER(fq_act_q), I32, I32, P, P, P,
+                                      P, P]),
+        "fq_swiglu_bwd_ckpt": (st, [P, P, P, I32, P, I32, I32, I32, ctypes.POINTER(fq_act_q), P, P,
+                                    P, P, SZ, P]),
         "fq_workspace_bytes": (SZ, [I32, fq_shape, I32, I32]),
         "fq_last_error": (ctypes.c_char_p, []),
         "fq_abi_version": (I32, []),
@@ -177,6 +194,23 @@ class ActQ:
 
     def c(self) -> fq_act_q:
         return fq_act_q(self.fmt, _p(self.scale))
+
+
+@dataclasses.dataclass
+class StoredW:
+    """A weight stack in its stored (exported) form: fmt, group, codes
+    [E,N,K] packed (fmt NONE: the bf16 stack), and the format's scales."""
+    fmt: int
+    group: int = 0
+    codes: Optional[torch.Tensor] = None
+    scale: Optional[torch.Tensor] = None
+    scale_bytes: Optional[torch.Tensor] = None
+    zero_point_bytes: Optional[torch.Tensor] = None
+    global_scale: Optional[torch.Tensor] = None
+
+    def c(self) -> fq_stored_w:
+        return fq_stored_w(self.fmt, self.group, _p(self.codes), _p(self.scale),
+                           _p(self.scale_bytes), _p(self.zero_point_bytes), _p(self.global_scale))
 
 
 def _shape(E, N, K) -> fq_shape:
@@ -309,6 +343,38 @@ def fq_dequantize_stacked(codes, shape, fmt, group, w_bf16, scale=None, scale_by
     _check(_lib.fq_dequantize_stacked(_p(codes), _shape(*shape), int(fmt), int(group), _p(scale),
                                       _p(scale_bytes), _p(zero_point_bytes), _p(global_scale),
                                       _p(w_bf16), _stream()))
+
+
+def fq_moe_tokens(x, T, H, F, expert_ids, probs, topk, expert_begin, E_local, w_gu: StoredW,
+                  w_d: StoredW, aq1: Optional[ActQ], aq2: Optional[ActQ], out, ws=None):
+    _check(_lib.fq_moe_tokens(_p(x), int(T), int(H), int(F), _p(expert_ids), _p(probs), int(topk),
+                              int(expert_begin), int(E_local), ctypes.byref(w_gu.c()),
+                              ctypes.byref(w_d.c()), _aq(aq1), _aq(aq2), _p(out), _p(ws),
+                              _nbytes(ws), _stream()))
+
+
+def fq_ckpt_save(x, rows, K, n_rows, fmt, group, codes, scale):
+    _check(_lib.fq_ckpt_save(_p(x), int(rows), int(K), _p(n_rows), int(fmt), int(group), _p(codes),
+                             _p(scale), _stream()))
+
+
+def fq_ckpt_load(codes, scale, rows, K, n_rows, fmt, group, x):
+    _check(_lib.fq_ckpt_load(_p(codes), _p(scale), int(rows), int(K), _p(n_rows), int(fmt),
+                             int(group), _p(x), _stream()))
+
+
+def fq_swiglu_actfq_ckpt(h, R_max, n_rows, F, aq: Optional[ActQ], fmt, group, a, aq_out, codes,
+                         scale):
+    _check(_lib.fq_swiglu_actfq_ckpt(_p(h), int(R_max), _p(n_rows), int(F), _aq(aq), int(fmt),
+                                     int(group), _p(a), _p(aq_out), _p(codes), _p(scale),
+                                     _stream()))
+
+
+def fq_swiglu_bwd_ckpt(daq, codes, scale, R_max, n_rows, F, fmt, group, aq: Optional[ActQ], dh,
+                       aq_out=None, dscale_a=None, ws=None):
+    _check(_lib.fq_swiglu_bwd_ckpt(_p(daq), _p(codes), _p(scale), int(R_max), _p(n_rows), int(F),
+                                   int(fmt), int(group), _aq(aq), _p(dh), _p(aq_out), _p(dscale_a),
+                                   _p(ws), _nbytes(ws), _stream()))
 
 
 def fq_topk_kl(student, teacher, T, V, K, reverse, valid, topk_idx, grad, loss_tok, loss_mean, ws):

@@ -184,6 +184,48 @@ fq_status check_dscale_a(const char *fn, const fq_act_q *aq, long rows, int cols
   return FQ_OK;
 }
 
+// One stored stack [E, N, K] of fq_moe_tokens.
+fq_status check_stored_w(const char *what, const fq_stored_w *w, int N, int K) {
+  FQ_CHECK_ARG(w != nullptr, "%s is NULL", what);
+  FQ_CHECK_ARG(w->fmt == FQ_FMT_NONE || valid_weight_fmt(w->fmt), "%s: unsupported format %d", what,
+               w->fmt);
+  FQ_CHECK_ARG(w->codes && aligned16(w->codes), "%s: codes must be non-NULL, 16-byte aligned", what);
+  if (w->fmt == FQ_FMT_NONE) return FQ_OK;
+  fq_weight_q q{w->fmt, w->group, nullptr, nullptr, nullptr};
+  FQ_TRY(check_weight_q(&q, {1, N, K}, false));
+  if (w->fmt == FQ_FMT_NVFP4) {
+    FQ_CHECK_ARG(w->scale_bytes && w->global_scale, "%s: nvfp4 needs scale_bytes and global_scale",
+                 what);
+    FQ_CHECK_ARG((reinterpret_cast<uintptr_t>(w->scale_bytes) & 1u) == 0,
+                 "%s: scale_bytes must be 2-byte aligned", what);
+    return FQ_OK;
+  }
+  FQ_CHECK_ARG(w->scale != nullptr, "%s: scale is NULL", what);
+  if (w->fmt == FQ_FMT_INT4) {
+    FQ_CHECK_ARG(w->zero_point_bytes != nullptr, "%s: int4 needs zero_point_bytes", what);
+    FQ_CHECK_SUPPORTED(w->group == K || w->group % 32 == 0,
+                       "%s: int4 groups are the row or a multiple of 32 (group=%d)", what, w->group);
+  }
+  return FQ_OK;
+}
+
+// An 8-bit checkpoint of [rows, K] with groups that must divide gdim.
+fq_status check_ckpt(int64_t rows, int64_t K, int gdim, int fmt, int group, const void *codes,
+                     const void *scale) {
+  FQ_CHECK_ARG(rows >= 0 && K > 0 && K % 16 == 0, "bad sizes (rows=%lld K=%lld; K %% 16 == 0)",
+               (long long)rows, (long long)K);
+  FQ_CHECK_ARG(rows * K < (1ll << 34), "too many elements");
+  FQ_CHECK_ARG(fmt == FQ_FMT_INT8 || fmt == FQ_FMT_FP8_E4M3,
+               "a checkpoint is int8 or fp8 (fmt %d)", fmt);
+  FQ_CHECK_ARG(group >= 16 && group <= 512 && (group & (group - 1)) == 0,
+               "checkpoint group %d must be a power of two from 16 to 512", group);
+  FQ_CHECK_ARG(gdim % group == 0, "checkpoint group %d must divide %d", group, gdim);
+  FQ_CHECK_ARG(rows == 0 || (codes && scale), "NULL pointer");
+  FQ_CHECK_ARG(!codes || aligned16(codes), "codes must be 16-byte aligned");
+  FQ_CHECK_ARG((reinterpret_cast<uintptr_t>(scale) & 3u) == 0, "scale must be 4-byte aligned");
+  return FQ_OK;
+}
+
 }  // namespace
 }  // namespace fq
 
@@ -202,6 +244,11 @@ size_t fq_workspace_bytes(int32_t op, fq_shape shape, int32_t R_max, int32_t fmt
   if (op == FQ_OP_ACT_SCALE_GRAD) {
     if (shape.N < 0 || shape.K <= 0) return 0;
     return align_up((size_t)act_grad_partials(shape.N, shape.K) * sizeof(float));
+  }
+  if (op == FQ_OP_MOE_TOKENS) {
+    if (fmts <= 0 || R_max < 0 || R_max % fmts || shape.E <= 0 || shape.N <= 0 || shape.K <= 0)
+      return 0;
+    return moe_tokens_ws_bytes(R_max / fmts, fmts, shape.E, shape.N, shape.K);
   }
   return 0;
 }
@@ -764,6 +811,94 @@ fq_status fq_moe_unpermute_reduce(const uint16_t *dxq, const int32_t *row_of, co
   launch_unpermute_reduce(dxq, row_of, x, T, topk, H, act_fmt(aq), aq ? aq->scale : nullptr, dx,
                           dscale_a, static_cast<float *>(ws), S(stream));
   FQ_CHECK_LAUNCH("fq_moe_unpermute_reduce");
+  return FQ_OK;
+}
+
+fq_status fq_moe_tokens(const uint16_t *x, int32_t T, int32_t H, int32_t F, const int32_t *ids,
+                        const float *probs, int32_t topk, int32_t ebegin, int32_t E,
+                        const fq_stored_w *w_gu, const fq_stored_w *w_d, const fq_act_q *aq1,
+                        const fq_act_q *aq2, uint16_t *out, void *ws, size_t ws_bytes,
+                        fq_stream stream) {
+  FQ_CHECK_ARG(T >= 0 && H > 0 && F > 0 && topk > 0 && E > 0,
+               "bad sizes (T=%d H=%d F=%d topk=%d E=%d)", T, H, F, topk, E);
+  FQ_CHECK_ARG(ebegin >= 0 && ebegin <= INT32_MAX - E, "bad expert_begin %d", ebegin);
+  FQ_CHECK_SUPPORTED(T <= kTokMax, "fq_moe_tokens takes up to %d tokens (T=%d)", kTokMax, T);
+  FQ_CHECK_SUPPORTED(topk <= 64 && E <= 1024, "topk <= 64 and E_local <= 1024 (topk=%d E=%d)", topk,
+                     E);
+  FQ_CHECK_SUPPORTED(H % 16 == 0 && F % 16 == 0 && H <= 16384 && F <= 16384,
+                     "H and F must be multiples of 16 up to 16384 (H=%d F=%d)", H, F);
+  FQ_TRY(check_stored_w("w_gu", w_gu, 2 * F, H));
+  FQ_TRY(check_stored_w("w_d", w_d, H, F));
+  FQ_TRY(check_act_q(aq1, H));
+  FQ_TRY(check_act_q(aq2, F));
+  FQ_CHECK_ARG(T == 0 || (x && ids && probs && out), "NULL pointer");
+  FQ_CHECK_ARG((!x || aligned16(x)) && (!out || aligned16(out)),
+               "bf16 tensors must be 16-byte aligned");
+  if (T == 0) return FQ_OK;
+  const size_t need = moe_tokens_ws_bytes(T, topk, E, H, F);
+  if (!ws || ws_bytes < need) {
+    set_error("fq_moe_tokens: workspace %zu bytes < %zu needed", ws_bytes, need);
+    return FQ_ERR_WORKSPACE_TOO_SMALL;
+  }
+  FQ_CHECK_ARG(aligned16(ws), "the workspace must be 16-byte aligned");
+  launch_moe_tokens(x, T, H, F, ids, probs, topk, ebegin, E, *w_gu, *w_d, act_fmt(aq1),
+                    aq1 ? aq1->scale : nullptr, act_fmt(aq2), aq2 ? aq2->scale : nullptr, out, ws,
+                    S(stream));
+  FQ_CHECK_LAUNCH("fq_moe_tokens");
+  return FQ_OK;
+}
+
+fq_status fq_ckpt_save(const uint16_t *x, int32_t rows, int32_t K, const int32_t *n_rows,
+                       int32_t fmt, int32_t group, uint8_t *codes, float *scale, fq_stream stream) {
+  FQ_TRY(check_ckpt(rows, K, K, fmt, group, codes, scale));
+  FQ_CHECK_ARG(rows == 0 || x, "x is NULL");
+  FQ_CHECK_ARG(!x || aligned16(x), "bf16 tensors must be 16-byte aligned");
+  launch_ckpt_save(x, rows, K, n_rows, fmt, group, codes, scale, S(stream));
+  FQ_CHECK_LAUNCH("fq_ckpt_save");
+  return FQ_OK;
+}
+
+fq_status fq_ckpt_load(const uint8_t *codes, const float *scale, int32_t rows, int32_t K,
+                       const int32_t *n_rows, int32_t fmt, int32_t group, uint16_t *x,
+                       fq_stream stream) {
+  FQ_TRY(check_ckpt(rows, K, K, fmt, group, codes, scale));
+  FQ_CHECK_ARG(rows == 0 || x, "x is NULL");
+  FQ_CHECK_ARG(!x || aligned16(x), "bf16 tensors must be 16-byte aligned");
+  launch_ckpt_load(codes, scale, rows, K, n_rows, fmt, group, x, S(stream));
+  FQ_CHECK_LAUNCH("fq_ckpt_load");
+  return FQ_OK;
+}
+
+fq_status fq_swiglu_actfq_ckpt(const uint16_t *h, int32_t R_max, const int32_t *n_rows, int32_t F,
+                               const fq_act_q *aq, int32_t fmt, int32_t group, uint16_t *a,
+                               uint16_t *aqo, uint8_t *codes, float *scale, fq_stream stream) {
+  FQ_CHECK_ARG(F > 0 && F % 16 == 0, "bad sizes (F must be a multiple of 16)");
+  FQ_TRY(check_ckpt(R_max, 2 * (int64_t)F, F, fmt, group, codes, scale));
+  FQ_CHECK_ARG(n_rows && (R_max == 0 || (h && aqo)), "NULL pointer");
+  FQ_CHECK_ARG((!h || aligned16(h)) && (!a || aligned16(a)) && (!aqo || aligned16(aqo)),
+               "bf16 tensors must be 16-byte aligned");
+  FQ_TRY(check_act_q(aq, F));
+  launch_swiglu_actfq_ckpt(h, R_max, n_rows, F, act_fmt(aq), aq ? aq->scale : nullptr, fmt, group,
+                           a, aqo, codes, scale, S(stream));
+  FQ_CHECK_LAUNCH("fq_swiglu_actfq_ckpt");
+  return FQ_OK;
+}
+
+fq_status fq_swiglu_bwd_ckpt(const uint16_t *daq, const uint8_t *codes, const float *scale,
+                             int32_t R_max, const int32_t *n_rows, int32_t F, int32_t fmt,
+                             int32_t group, const fq_act_q *aq, uint16_t *dh, uint16_t *aqo,
+                             float *dscale_a, void *ws, size_t ws_bytes, fq_stream stream) {
+  FQ_CHECK_ARG(F > 0 && F % 16 == 0, "bad sizes (F must be a multiple of 16)");
+  FQ_TRY(check_ckpt(R_max, 2 * (int64_t)F, F, fmt, group, codes, scale));
+  FQ_CHECK_ARG(n_rows && (R_max == 0 || (daq && dh)), "NULL pointer");
+  FQ_CHECK_ARG((!daq || aligned16(daq)) && (!dh || aligned16(dh)) && (!aqo || aligned16(aqo)),
+               "bf16 tensors must be 16-byte aligned");
+  FQ_TRY(check_act_q(aq, F));
+  if (dscale_a) FQ_TRY(check_dscale_a("fq_swiglu_bwd_ckpt", aq, R_max, F, ws, ws_bytes));
+  launch_swiglu_bwd_ckpt(daq, codes, scale, R_max, n_rows, F, fmt, group, act_fmt(aq),
+                         aq ? aq->scale : nullptr, dh, aqo, dscale_a, static_cast<float *>(ws),
+                         S(stream));
+  FQ_CHECK_LAUNCH("fq_swiglu_bwd_ckpt");
   return FQ_OK;
 }
 

@@ -46,6 +46,32 @@ void launch_unpermute_reduce(const uint16_t *dxq, const int32_t *row_of, const u
                              int topk, int H, int afmt, const float *ascale, uint16_t *dx,
                              float *dscale_a, float *part, hipStream_t st);
 
+// out[0] = sum of n floats in a fixed order
+void launch_sum_partials(const float *part, uint32_t n, float *out, hipStream_t st);
+
+// activation checkpoints in 8 bits (fmt INT8 or FP8_E4M3; group a power of two
+// from 16 to 512 that divides the row, resp. F). n_rows as in launch_act_fq.
+void launch_ckpt_save(const uint16_t *x, int rows, int K, const int32_t *n_rows, int fmt, int group,
+                      uint8_t *codes, float *scale, hipStream_t st);
+void launch_ckpt_load(const uint8_t *codes, const float *scale, int rows, int K,
+                      const int32_t *n_rows, int fmt, int group, uint16_t *x, hipStream_t st);
+void launch_swiglu_actfq_ckpt(const uint16_t *h, int R_max, const int32_t *n_rows, int F, int afmt,
+                              const float *ascale, int fmt, int group, uint16_t *a, uint16_t *aq,
+                              uint8_t *codes, float *scale, hipStream_t st);
+// aq, dscale_a may be NULL; part: act_grad_partials floats with dscale_a
+void launch_swiglu_bwd_ckpt(const uint16_t *daq, const uint8_t *codes, const float *scale,
+                            int R_max, const int32_t *n_rows, int F, int fmt, int group, int afmt,
+                            const float *ascale, uint16_t *dh, uint16_t *aq, float *dscale_a,
+                            float *part, hipStream_t st);
+
+// One MoE layer for T <= kTokMax tokens over stored weights (workspace bytes below).
+constexpr int kTokMax = 128;
+size_t moe_tokens_ws_bytes(int T, int topk, int E, int H, int F);
+void launch_moe_tokens(const uint16_t *x, int T, int H, int F, const int32_t *ids,
+                       const float *probs, int topk, int ebegin, int E, const fq_stored_w &w_gu,
+                       const fq_stored_w &w_d, int afmt1, const float *as1, int afmt2,
+                       const float *as2, uint16_t *out, void *ws, hipStream_t st);
+
 // real-quantized export: E4M3 bytes of clamp(theta, 0, 448); zero-point bytes;
 // decode of stored codes + scales to bf16 (group = N*K for one scale per matrix)
 void launch_export_theta(const float *theta, size_t n, uint8_t *out, hipStream_t st);

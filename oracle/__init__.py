@@ -84,3 +84,7 @@ from .moe import (  # noqa: F401
     gather_actfq, swiglu_fwd, swiglu_actfq, swiglu_bwd, combine, combine_bwd,
     unpermute_reduce, unpermute_sum, act_scale_grad, moe_layer, teacher_forward,
 )
+from .ckpt import (  # noqa: F401
+    CKPT_D, ckpt_save, ckpt_load, ckpt_values, swiglu_from_values, swiglu_bwd_values, a_bits_of,
+)
+from .moe_tokens import moe_tokens, stored_values  # noqa: F401
