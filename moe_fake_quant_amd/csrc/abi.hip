@@ -248,7 +248,7 @@ size_t fq_workspace_bytes(int32_t op, fq_shape shape, int32_t R_max, int32_t fmt
   if (op == FQ_OP_MOE_TOKENS) {
     if (fmts <= 0 || R_max < 0 || R_max % fmts || shape.E <= 0 || shape.N <= 0 || shape.K <= 0)
       return 0;
-    return moe_tokens_ws_bytes(R_max / fmts, fmts, shape.E, shape.N, shape.K);
+    return moe_tokens_ws_bytes(R_max / fmts, fmts, shape.E, shape.K);
   }
   return 0;
 }
@@ -835,7 +835,7 @@ fq_status fq_moe_tokens(const uint16_t *x, int32_t T, int32_t H, int32_t F, cons
   FQ_CHECK_ARG((!x || aligned16(x)) && (!out || aligned16(out)),
                "bf16 tensors must be 16-byte aligned");
   if (T == 0) return FQ_OK;
-  const size_t need = moe_tokens_ws_bytes(T, topk, E, H, F);
+  const size_t need = moe_tokens_ws_bytes(T, topk, E, F);
   if (!ws || ws_bytes < need) {
     set_error("fq_moe_tokens: workspace %zu bytes < %zu needed", ws_bytes, need);
     return FQ_ERR_WORKSPACE_TOO_SMALL;
