@@ -488,6 +488,7 @@ fq_status fq_moe_unpermute_reduce(const uint16_t *dxq_bf16, const int32_t *row_o
  *   scale_bytes and global_scale (nvfp4), zero_point_bytes (int4).
  *   w_gu is [E_local, 2F, H], w_d [E_local, H, F]; their formats may differ.
  * x_bf16, out_bf16 [T, H]; expert_ids, probs [T, topk]. out must not overlap x.
+ * codes and the scale pointers 16-byte aligned (global_scale: 4-byte).
  * 0 <= T <= 128 (for more tokens the grouped GEMM calls are the path),
  * 1 <= topk <= 64, E_local <= 1024, H and F % 16 == 0 and <= 16384.
  * Workspace: fq_workspace_bytes(FQ_OP_MOE_TOKENS, {E_local, H, F}, T * topk,

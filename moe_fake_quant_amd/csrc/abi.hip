@@ -196,13 +196,13 @@ fq_status check_stored_w(const char *what, const fq_stored_w *w, int N, int K) {
   if (w->fmt == FQ_FMT_NVFP4) {
     FQ_CHECK_ARG(w->scale_bytes && w->global_scale, "%s: nvfp4 needs scale_bytes and global_scale",
                  what);
-    FQ_CHECK_ARG((reinterpret_cast<uintptr_t>(w->scale_bytes) & 1u) == 0,
-                 "%s: scale_bytes must be 2-byte aligned", what);
+    FQ_CHECK_ARG(aligned16(w->scale_bytes), "%s: scale_bytes must be 16-byte aligned", what);
     return FQ_OK;
   }
-  FQ_CHECK_ARG(w->scale != nullptr, "%s: scale is NULL", what);
+  FQ_CHECK_ARG(w->scale && aligned16(w->scale), "%s: scale must be non-NULL, 16-byte aligned", what);
   if (w->fmt == FQ_FMT_INT4) {
-    FQ_CHECK_ARG(w->zero_point_bytes != nullptr, "%s: int4 needs zero_point_bytes", what);
+    FQ_CHECK_ARG(w->zero_point_bytes && aligned16(w->zero_point_bytes),
+                 "%s: int4 needs zero_point_bytes, 16-byte aligned", what);
     FQ_CHECK_SUPPORTED(w->group == K || w->group % 32 == 0,
                        "%s: int4 groups are the row or a multiple of 32 (group=%d)", what, w->group);
   }

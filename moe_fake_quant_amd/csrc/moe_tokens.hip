@@ -73,104 +73,110 @@ struct TokStack {  // one projection's stored weights
   int nch;                  // chunks per row
   int whole;                // rows are whole chunks
   int f16;                  // operands are f16 (NVFP4 with quantized activations)
+  int seg;                  // Fmt::kSeg
   FastDiv dgroup;           // / group
 };
+
+// The scales of an item's rows pass through LDS: the rows of a tile lie behind
+// one another, so they are fetched in whole cache lines, where a load per lane
+// and segment would touch 16 lines for a few bytes of each (and took as long as
+// the load of the segment's codes). A row's bytes, and its distance in LDS
+// (8 more, so that a column of rows falls into different banks).
+struct RowBytes {
+  int n, stride;
+  FastDiv per8, per1;  // / 8-byte units, / bytes of a row
+};
+inline RowBytes row_bytes(int n) {
+  RowBytes r;
+  r.n = n;
+  r.stride = (n + 7) / 8 * 8 + 8;
+  r.per8 = FastDiv((uint32_t)(n >= 8 ? n / 8 : 1));
+  r.per1 = FastDiv((uint32_t)(n > 0 ? n : 1));
+  return r;
+}
 
 struct TokArgs {
   const uint16_t *x;        // [T, H]
   const int32_t *ids;       // [T, topk]
   const float *probs;       // [T, topk]
-  int T, topk, P, ebegin, E, slots;
+  int T, topk, P, ebegin, E;
   FastDiv dtopk;
   int afmt1, afmt2;
   const float *as1, *as2;
   TokStack gu, d;
   int H, F;
   int ncol;                 // columns (tokens) staged at a time by the gate_up kernel
+  int ny;                   // channel blocks of a gate_up expert
+  FastDiv dny;
   FastDiv dvpr;             // / 8-element vectors of a staged token row
-  // workspace. Rows are ordered by expert; a slot's rows are off .. off + cnt - 1.
-  uint16_t *a;              // [P, F] A's grid values
-  int2 *span;               // [slots] {off, cnt} (cnt 0: nothing to do)
+  int idb, xb;              // gate_up LDS: bytes of the ids, of the staged rows
+  RowBytes rsc, rzp;        // gate_up: scale (or scale byte) and zero point bytes of a row
+  int agroups, arow;        // A's 16-channel groups and row length, padded to whole chunks
+  // workspace. Rows are the pairs in expert order.
+  uint16_t *a;              // [P, arow] A's grid values, in MFMA step order (see a_index)
+  int4 *act;                // [min(P, E)] the experts with rows: {expert, first row, rows, 0}
+  int32_t *nact;            // their number
   int32_t *tok;             // [P] a row's token
   float *pw;                // [P] its weight
   uint16_t *out;
 };
 
-// The expert of a slot: with fewer pairs than experts a slot is a pair (and
-// only the first pair that names an expert does its work), else an expert.
-__device__ __forceinline__ int local_id(const TokArgs &a, int q) {  // wraps, never overflows
-  return (int)((uint32_t)a.ids[q] - (uint32_t)a.ebegin);
-}
-__device__ __forceinline__ int slot_expert(const TokArgs &a, int slot) {
-  if (a.P >= a.E) return slot;
-  const int e = local_id(a, slot);
-  return (unsigned)e < (unsigned)a.E ? e : -1;
-}
-
 // ------------------------------------------------------------ weight codes --
-struct Raw {
+struct Codes {
   uint32_t w[4];
-  uint32_t sb;   // NVFP4: the block scale bytes of the segment's two 16-blocks
-  float s0, zp;  // kPre: the segment's scale; INT4: its zero point
+};
+struct Scales {  // of one segment
+  uint32_t sb;   // NVFP4: the block scale bytes of its two 16-blocks
+  float s0, zp;  // kPre: its scale; INT4: its zero point
 };
 
-// One lane's row, from the lane's segment of chunk 0 on. A chunk is 64 bytes of
-// codes in every format (4 lane groups x 16 bytes).
-struct RowPtr {
-  const uint8_t *c, *sb, *zp;
-  const float *sc;
-};
-template <int FMT, int MODE>
-__device__ __forceinline__ RowPtr row_ptr(const TokStack &t, size_t row, int kq) {
-  RowPtr p;
-  const size_t bytes = FMT == FQ_FMT_NONE ? (size_t)t.K * 2
-                       : Fmt<FMT>::k4bit ? (size_t)t.K / 2 : (size_t)t.K;
-  p.c = t.codes + row * bytes + kq * 16;
-  p.sb = FMT == FQ_FMT_NVFP4 ? t.sbytes + row * (size_t)(t.K >> 4) + kq * 2 : nullptr;
-  p.zp = FMT == FQ_FMT_INT4 ? t.zp + row * (size_t)t.groups : nullptr;
-  p.sc = MODE == kPre && FMT != FQ_FMT_NVFP4 ? t.scale + row * (size_t)t.groups : nullptr;
-  return p;
+__device__ __forceinline__ const uint8_t *row_codes(const TokStack &t, int fmt4, size_t row,
+                                                    int kq) {
+  const size_t bytes = fmt4 == 0 ? (size_t)t.K * 2 : fmt4 == 2 ? (size_t)t.K / 2 : (size_t)t.K;
+  return t.codes + row * bytes + kq * 16;
+}
+template <int FMT>
+__device__ __forceinline__ const uint8_t *row_codes(const TokStack &t, size_t row, int kq) {
+  return row_codes(t, FMT == FQ_FMT_NONE ? 0 : Fmt<FMT>::k4bit ? 2 : 1, row, kq);
 }
 
-// The lane's segment of chunk ch. Past the end of the row nothing is read and
-// the codes are 0 (what they meet there is 0 too).
-template <int FMT, int MODE>
-__device__ __forceinline__ Raw load_raw(const TokStack &t, const RowPtr &p, int ch, int kq) {
-  const int k0 = ch * Fmt<FMT>::kChunk + kq * Fmt<FMT>::kSeg;
-  Raw r;
-  if (t.whole) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(p.c + ch * 64);
+// The lane's segment of chunk ch of a row (p: row_codes; a chunk is 64 bytes in
+// every format, 4 lane groups x 16 bytes). Past the end of the row nothing is
+// read and the codes are 0 (what they meet there is 0 too).
+template <int FMT, bool WHOLE>
+__device__ __forceinline__ Codes load_codes(const TokStack &t, const uint8_t *p, int ch, int kq) {
+  Codes r;
+  p += ch * 64;
+  if (WHOLE) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
     r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
-    if (FMT == FQ_FMT_NVFP4) r.sb = *reinterpret_cast<const uint16_t *>(p.sb + ch * 8);
-  } else {
-    r.w[0] = r.w[1] = r.w[2] = r.w[3] = r.sb = 0u;
-    r.s0 = r.zp = 0.0f;
-    if (k0 >= t.K) return r;
-    const uint8_t *c = p.c + ch * 64;
-    if (Fmt<FMT>::k4bit && (t.K & 31)) {
-      // rows are multiples of 8 bytes, the last segment may hold 16 codes
-      const uint2 v = *reinterpret_cast<const uint2 *>(c);
-      r.w[0] = v.x; r.w[1] = v.y;
-      if (k0 + 16 < t.K) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(c + 8);
-        r.w[2] = u.x; r.w[3] = u.y;
-      }
-    } else {
-      const uint4 v = *reinterpret_cast<const uint4 *>(c);
-      r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
-    }
-    if (FMT == FQ_FMT_NVFP4) {
-      const uint8_t *b = p.sb + ch * 8;
-      r.sb = (uint32_t)b[0] | (k0 + 16 < t.K ? (uint32_t)b[1] << 8 : 0u);
-    }
+    return r;
   }
-  if (FMT == FQ_FMT_INT4 || (MODE == kPre && FMT != FQ_FMT_NVFP4)) {
-    const uint32_t gi = t.dgroup.div((uint32_t)k0);
-    if (MODE == kPre) r.s0 = p.sc[gi];
-    if (FMT == FQ_FMT_INT4) r.zp = (float)p.zp[gi];
+  const int k0 = ch * Fmt<FMT>::kChunk + kq * Fmt<FMT>::kSeg;
+  r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0u;
+  if (k0 >= t.K) return r;
+  if (Fmt<FMT>::k4bit && (t.K & 31)) {
+    // rows are multiples of 8 bytes, the last segment may hold 16 codes
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    r.w[0] = v.x; r.w[1] = v.y;
+    if (k0 + 16 < t.K) {
+      const uint2 u = *reinterpret_cast<const uint2 *>(p + 8);
+      r.w[2] = u.x; r.w[3] = u.y;
+    }
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
   }
   return r;
 }
+
+// Does a format and mode have scales (sb or s0) / zero points per segment?
+template <int FMT, int MODE>
+struct Has {
+  static constexpr bool kSb = FMT == FQ_FMT_NVFP4;
+  static constexpr bool kS = FMT != FQ_FMT_NONE && FMT != FQ_FMT_NVFP4 && MODE != kEnd;
+  static constexpr bool kZp = FMT == FQ_FMT_INT4;
+};
 
 // One MFMA over step st of a chunk: 8 consecutive elements of the lane's row
 // against the 8 activation grid values in x (bf16, or f16 with F16).
@@ -181,10 +187,11 @@ __device__ __forceinline__ Raw load_raw(const TokStack &t, const RowPtr &p, int 
 // value exactly (at most 8 bits, 2^-10 <= |v| <= 2688), but not any bf16
 // activation, so it is used for quantized activations.
 template <int FMT, int MODE, bool F16>
-__device__ __forceinline__ f32x4 mfma_step(const Raw &r, int st, const bf16x8_t &x, f32x4 acc) {
+__device__ __forceinline__ f32x4 mfma_step(const Codes &r, const Scales &q, int st,
+                                           const bf16x8_t &x, f32x4 acc) {
   if (FMT == FQ_FMT_NVFP4 && F16) {
     const uint32_t c = r.w[st];
-    const f16x2 th = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.sb, 1.0f, false);
+    const f16x2 th = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q.sb, 1.0f, false);
     const _Float16 s = st < 2 ? th.x : th.y;
     const f16x2 ss = {s, s};
     f16x2 v[4];
@@ -211,7 +218,7 @@ __device__ __forceinline__ f32x4 mfma_step(const Raw &r, int st, const bf16x8_t 
     float v[8];
     if (FMT == FQ_FMT_NVFP4) {
       const uint32_t c = r.w[st];
-      const f32x2_t th = __builtin_amdgcn_cvt_pk_f32_fp8(r.sb, false);
+      const f32x2_t th = __builtin_amdgcn_cvt_pk_f32_fp8(q.sb, false);
       const float s = st < 2 ? th.x : th.y;
       const f32x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0);
       const f32x2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
@@ -224,8 +231,8 @@ __device__ __forceinline__ f32x4 mfma_step(const Raw &r, int st, const bf16x8_t 
       const uint32_t ev = r.w[st] & 0x0F0F0F0Fu, od = (r.w[st] >> 4) & 0x0F0F0F0Fu;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        v[2 * j] = (float)((ev >> (8 * j)) & 0xFFu) - r.zp;
-        v[2 * j + 1] = (float)((od >> (8 * j)) & 0xFFu) - r.zp;
+        v[2 * j] = (float)((ev >> (8 * j)) & 0xFFu) - q.zp;
+        v[2 * j + 1] = (float)((od >> (8 * j)) & 0xFFu) - q.zp;
       }
     } else {
 #pragma unroll
@@ -243,22 +250,12 @@ __device__ __forceinline__ f32x4 mfma_step(const Raw &r, int st, const bf16x8_t 
     }
     if (FMT != FQ_FMT_NVFP4 && MODE == kPre) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = v[j] * r.s0;
+      for (int j = 0; j < 8; ++j) v[j] = v[j] * q.s0;
     }
     o = pack8(v);
   }
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8v, o),
                                                  __builtin_bit_cast(bf16x8v, x), acc, 0, 0, 0);
-}
-
-// kPost: the chunk's scales of the four rows a lane holds of a result tile
-template <int FMT>
-__device__ __forceinline__ f32x4 chunk_scales(const TokStack &t, size_t row0, int chunk) {
-  const float *p = t.scale + row0 * t.groups + t.dgroup.div((uint32_t)(chunk * Fmt<FMT>::kChunk));
-  f32x4 s;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) s[i] = p[(size_t)i * t.groups];
-  return s;
 }
 
 // the factor of a finished sum of one row of expert e
@@ -314,65 +311,104 @@ __host__ __device__ inline int xrow_bytes(int K, int chunk) {
 
 extern __shared__ __attribute__((aligned(16))) char g_tok_lds[];
 
-// A slot's rows: its expert's pairs in ascending order, a pair that repeats an
-// expert of its token left to the first one (which takes the summed weight).
-struct SlotRows {
-  int32_t tok[128];
+// The plan of a batch, made by every gate_up block for itself (it costs less
+// than waiting for another kernel): rows = the local pairs in expert order,
+// within an expert in pair order, a pair that repeats an expert of its token
+// left to the first one (which takes the summed weight).
+constexpr uint16_t kNoId = 0x7FFF;   // not local
+constexpr uint16_t kRepeat = 0x8000;
+struct Plan {
+  int cnt[1024];       // rows of an expert
+  uint16_t off[1024];  // its first row
+  uint16_t act[1024];  // the experts with rows, ascending
+  uint32_t wsum[kWaves];
+  int32_t tok[128];    // tokens of the current expert's rows
   float pw[128];
-  int32_t ids[kNT];
-  int wcnt[2][kWaves];
-  int first;
+  int wcnt[kWaves];
 };
 
-// Fills r (LDS) for expert e and returns the number of rows; `off`: the rows of
-// experts below e come before; `first`: the pair of the first row (P: none).
-__device__ __forceinline__ int build_rows(const TokArgs &a, int e, SlotRows &r, int &off,
-                                          int &first) {
+// ids: LDS, P entries: the pair's local expert | kRepeat. Returns the number of
+// experts with rows.
+__device__ __forceinline__ int make_plan(const TokArgs &a, Plan &p, uint16_t *ids) {
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int per = (int)a.dtopk.div((uint32_t)kNT) * a.topk;  // whole tokens per pass
-  int n = 0;
-  off = 0;
-  first = a.P;
-  for (int q0 = 0; q0 < a.P; q0 += per) {
-    const int q = q0 + tid;
-    const bool in = tid < per && q < a.P;
-    const int id = in ? local_id(a, q) : -1;
-    float p = in ? a.probs[q] : 0.0f;
-    r.ids[tid] = id;
-    // a pair below the expert takes a row, whether or not it repeats one
-    const uint64_t below = __ballot(id >= 0 && id < e);
+  for (int q = tid; q < a.P; q += kNT) {
+    const uint32_t id = (uint32_t)a.ids[q] - (uint32_t)a.ebegin;  // wraps, never overflows
+    ids[q] = id < (uint32_t)a.E ? (uint16_t)id : kNoId;
+  }
+  for (int e = tid; e < a.E; e += kNT) p.cnt[e] = 0;
+  __syncthreads();
+  uint32_t repeat = 0;  // one bit per pair of this thread (P <= 128 * 64 = 16 kNT)
+  for (int q = tid, k = 0; q < a.P; q += kNT, ++k) {
+    const uint16_t id = ids[q];
+    if (id == kNoId) continue;
+    bool again = false;
+    for (int i = (int)a.dtopk.div((uint32_t)q) * a.topk; i < q; ++i) again |= ids[i] == id;
+    if (again) repeat |= 1u << k;
+    else atomicAdd(&p.cnt[id], 1);
+  }
+  __syncthreads();
+  for (int q = tid, k = 0; q < a.P; q += kNT, ++k)
+    if ((repeat >> k) & 1u) ids[q] |= kRepeat;
+  // prefix sums over the experts, rows in the low half, experts with rows in the high
+  uint32_t run = 0;
+  for (int e0 = 0; e0 < a.E; e0 += kNT) {
+    const int e = e0 + tid;
+    const int c = e < a.E ? p.cnt[e] : 0;
+    const uint32_t v = (uint32_t)c | (c > 0 ? 0x10000u : 0u);
+    uint32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t y = __shfl_up(x, o, 64);
+      if (lane >= o) x += y;
+    }
+    if (lane == 63) p.wsum[wave] = x;
     __syncthreads();
-    bool hit = in && id == e;
-    const int t = (int)a.dtopk.div((uint32_t)tid);
-    if (hit) {
-      for (int i = t * a.topk; i < tid; ++i)
-        if (r.ids[i] == e) hit = false;
-      if (hit)
-        for (int i = tid + 1; i < (t + 1) * a.topk; ++i)
-          if (r.ids[i] == e) p += a.probs[q0 + i];
+    uint32_t base = run;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) base += p.wsum[w];
+      run += p.wsum[w];
     }
+    if (c > 0) {
+      const uint32_t ex = base + x - v;
+      p.off[e] = (uint16_t)(ex & 0xFFFFu);
+      p.act[ex >> 16] = (uint16_t)e;
+    }
+    __syncthreads();
+  }
+  return (int)(run >> 16);
+}
+
+// The tokens (and, with_pw, the weights) of expert e's rows into p.tok / p.pw.
+__device__ __forceinline__ void list_rows(const TokArgs &a, Plan &p, const uint16_t *ids, int e,
+                                          bool with_pw) {
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  int n = 0;
+  for (int q0 = 0; q0 < a.P; q0 += kNT) {
+    const int q = q0 + tid;
+    const bool hit = q < a.P && ids[q] == (uint16_t)e;
     const uint64_t m = __ballot(hit);
-    if (lane == 0) {
-      r.wcnt[0][wave] = __popcll(m);
-      r.wcnt[1][wave] = __popcll(below);
-    }
+    if (lane == 0) p.wcnt[wave] = __popcll(m);
     __syncthreads();
     int base = n;
+#pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      if (w < wave) base += r.wcnt[0][w];
-      n += r.wcnt[0][w];
-      off += r.wcnt[1][w];
+      if (w < wave) base += p.wcnt[w];
+      n += p.wcnt[w];
     }
     if (hit) {
       const int i = base + __popcll(m & ((1ull << lane) - 1ull));
-      r.tok[i] = (int)a.dtopk.div((uint32_t)q);
-      r.pw[i] = p;
-      if (i == 0) r.first = q;
+      const int t = (int)a.dtopk.div((uint32_t)q);
+      p.tok[i] = t;
+      if (with_pw) {
+        float v = a.probs[q];
+        for (int j = q + 1; j < (t + 1) * a.topk; ++j)
+          if (ids[j] == (uint16_t)(e | kRepeat)) v += a.probs[j];
+        p.pw[i] = v;
+      }
     }
     __syncthreads();
-    if (n > 0) first = r.first;
   }
-  return n;
 }
 
 // One 8-element vector of a token row as grid values (the neighbouring lane
@@ -398,166 +434,286 @@ __device__ __forceinline__ bf16x8_t stage_vec(const ActQ &q, bf16x8_t o, float r
   return o;
 }
 
-// A block forms MT x 16 channels of A for one expert and its tokens. Its eight
-// waves are MT channel groups (gate and up rows of the same 16 channels) times
-// 8 / MT shares of the contraction. MT follows from the number of blocks: more
-// channels to a block spread the staging of the tokens over more weights, fewer
-// keep every CU busy for a handful of tokens (see launch_moe_tokens).
-template <int FMT, int MODE, bool F16, int MT>
+// Where channel f of A lies in its row: within a chunk of the down projection
+// the elements of one MFMA step are contiguous (step, lane group, 8 elements),
+// so that a step's operand is read in whole 64-byte pieces.
+template <int SEG>
+__device__ __forceinline__ int a_index(int f) {
+  const int in = f & (4 * SEG - 1);
+  return (f - in) + (in & (SEG - 1)) / 8 * 32 + in / SEG * 8 + (in & 7);
+}
+__device__ __forceinline__ int a_index(int seg, int f) {
+  return seg == 32 ? a_index<32>(f) : seg == 16 ? a_index<16>(f) : f;
+}
+
+// An item is MT x 16 channels of A for one expert and its tokens; a block takes
+// a contiguous share of the items in (expert, channels) order, so it stages an
+// expert's tokens once and streams the weights of several items past them. Its
+// eight waves are MT channel groups (gate and up rows of the same 16 channels)
+// times 8 / MT shares of the contraction. The first weights of an item are
+// requested before the sums of the one before are added up.
+template <int FMT, int MODE, bool F16, bool WHOLE, int MT>
 __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
   constexpr int kChunk = Fmt<FMT>::kChunk, kSeg = Fmt<FMT>::kSeg, kSteps = Fmt<FMT>::kSteps;
+  constexpr bool kSb = Has<FMT, MODE>::kSb, kS = Has<FMT, MODE>::kS, kZp = Has<FMT, MODE>::kZp;
   constexpr int kWK = kWaves / MT;
-  constexpr int kU = 2;  // chunks of a batch; one batch computes while the next loads
-  constexpr int kX = 2;  // token vectors a thread has in flight
-  __shared__ SlotRows rows;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int slot = blockIdx.x;
-
-  const int e = slot_expert(a, slot);
-  int first = a.P, n = 0, off = 0;
-  if (e >= 0) n = build_rows(a, e, rows, off, first);
-  if (a.P < a.E && first != slot) n = 0;
-  if (blockIdx.y == 0) {
-    if (tid == 0) a.span[slot] = make_int2(off, n);
-    if (tid < n) {
-      a.tok[off + tid] = rows.tok[tid];
-      a.pw[off + tid] = rows.pw[tid];
-    }
-  }
-  if (n == 0) return;
-
+  constexpr int kU = 2;   // chunks of a batch; one batch computes while the next loads
+  constexpr int kX = 2;   // token vectors a thread has in flight
+  constexpr int kOut = (MT * 256 + kNT - 1) / kNT;  // channels x columns per thread
+  __shared__ Plan plan;
+  uint16_t *ids = reinterpret_cast<uint16_t *>(g_tok_lds);
+  char *xrows = g_tok_lds + a.idb;
+  f32x4 *red = reinterpret_cast<f32x4 *>(g_tok_lds + a.idb + a.xb);
+  // scales and zero points of the item's rows: MT * 16 gate rows, then the up rows
+  char *scl = g_tok_lds + a.idb + a.xb + kRedBytes;
+  char *zpl = scl + (kSb || kS ? 2 * MT * kTile * a.rsc.stride : 0);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform: scalar loop control
   const TokStack &w = a.gu;
   const ActQ q1 = load_actq(a.afmt1, a.as1), q2 = load_actq(a.afmt2, a.as2);
-  const float rg1 = 1.0f / (6.0f * q1.s);
+
+  const int na = __builtin_amdgcn_readfirstlane(make_plan(a, plan, ids));
+  if (blockIdx.x == 0) {
+    if (tid == 0) a.nact[0] = na;
+    for (int i = tid; i < na; i += kNT) {
+      const int e = plan.act[i];
+      a.act[i] = make_int4(e, plan.off[e], plan.cnt[e], 0);
+    }
+  }
+  const uint32_t items = (uint32_t)(na * a.ny);
+  const int it0 = (int)((uint64_t)items * blockIdx.x / gridDim.x);
+  const int it1 = (int)((uint64_t)items * (blockIdx.x + 1) / gridDim.x);
+  if (it0 >= it1) return;
+
+  const float rg1 = 1.0f / (6.0f * q1.s), rg2 = 1.0f / (6.0f * q2.s);
   const int xstride = xrow_bytes(w.K, kChunk);
   const int col = lane & 15, kq = lane >> 4;
   const int wm = wave / kWK, wk = wave % kWK;
-  const int f0 = (blockIdx.y * MT + wm) * kTile;
-  const bool live_w = f0 < a.F;  // the last block's waves past F only stage and sync
-  const size_t row_g = (size_t)e * w.N + (live_w ? f0 : 0), row_u = row_g + a.F;
-  const RowPtr pg = row_ptr<FMT, MODE>(w, row_g + col, kq);
-  const RowPtr pu = row_ptr<FMT, MODE>(w, row_u + col, kq);
-  const int nch = live_w ? w.nch : 0;
   const int vpr = w.nch * kChunk / 8, live = w.K / 8;
 
-  Raw raw[2][kU][2];
-  auto load = [&](Raw (&r)[kU][2], int cb) {
+  Codes raw[2][kU][2];
+  const uint8_t *pg = nullptr, *pu = nullptr;
+  int nch = 0;
+  auto point = [&](int it) {  // this wave's rows of an item (none past F)
+    const int sl = (int)a.dny.div((uint32_t)it);
+    const int f0 = ((it - sl * a.ny) * MT + wm) * kTile;
+    nch = f0 < a.F ? w.nch : 0;
+    const size_t row0 =
+        (size_t)__builtin_amdgcn_readfirstlane(plan.act[sl]) * w.N + (f0 < a.F ? f0 : 0);
+    const size_t row = row0 + col;
+    pg = row_codes<FMT>(w, row, kq);
+    pu = row_codes<FMT>(w, row + a.F, kq);
+  };
+  auto load = [&](Codes (&r)[kU][2], int cb) {
 #pragma unroll
     for (int u = 0; u < kU; ++u)
-      if (cb + u * kWK < nch) {
-        r[u][0] = load_raw<FMT, MODE>(w, pg, cb + u * kWK, kq);
-        r[u][1] = load_raw<FMT, MODE>(w, pu, cb + u * kWK, kq);
+      if (cb + u < nch) {
+        r[u][0] = load_codes<FMT, WHOLE>(w, pg, cb + u, kq);
+        r[u][1] = load_codes<FMT, WHOLE>(w, pu, cb + u, kq);
       }
   };
-
-  for (int c0 = 0; c0 < n; c0 += a.ncol) {
-    const int nc = min(a.ncol, n - c0), nvec = nc * vpr;
-    // ---- the tokens' grid values into LDS, a row's vectors beyond K zero. The
-    // first weights are requested behind the first token vectors and arrive
-    // while those are quantized. (vpr is even: both lanes of a 16-block take
-    // part together.)
-    for (int i0 = 0; i0 < nvec; i0 += kX * kNT) {
-      bf16x8_t xv[kX];
-      int dst[kX];
-#pragma unroll
-      for (int j = 0; j < kX; ++j) {
-        const int i = i0 + j * kNT + tid;
-        const int c = (int)a.dvpr.div((uint32_t)i), v = i - c * vpr;
-        dst[j] = i < nvec ? c * xstride + v * 16 : -1;
-        xv[j] = {{0u, 0u, 0u, 0u}};
-        if (i < nvec && v < live)
-          xv[j] = reinterpret_cast<const bf16x8_t *>(a.x + (size_t)rows.tok[c0 + c] * w.K)[v];
+  // Rows of n bytes (a multiple of 8) are copied in 8-byte units: unit i of an
+  // item is unit i - r * n / 8 of its row r. Rows past F are left out.
+  const uint8_t *sbase = kSb ? w.sbytes : reinterpret_cast<const uint8_t *>(w.scale);
+  auto item_row = [&](int it, int r, size_t &row) {
+    const int sl = (int)a.dny.div((uint32_t)it);
+    const int f0 = (it - sl * a.ny) * MT * kTile, half = r >= MT * kTile;
+    const int f = f0 + r - half * MT * kTile;
+    row = (size_t)__builtin_amdgcn_readfirstlane(plan.act[sl]) * w.N + half * a.F + f;
+    return f < a.F;
+  };
+  const int units = a.rsc.n % 8 == 0 ? 2 * MT * kTile * (a.rsc.n / 8) : 0;
+  auto store_scales = [&](int it) {
+    if (kSb || kS) {
+#pragma unroll 2
+      for (int i = tid; i < units; i += kNT) {
+        const int r = (int)a.rsc.per8.div((uint32_t)i), o = (i - r * (a.rsc.n / 8)) * 8;
+        size_t row;
+        if (item_row(it, r, row))
+          *reinterpret_cast<uint2 *>(scl + r * a.rsc.stride + o) =
+              *reinterpret_cast<const uint2 *>(sbase + row * a.rsc.n + o);
       }
-      if (i0 == 0) load(raw[0], wk);
-#pragma unroll
-      for (int j = 0; j < kX; ++j)
-        if (dst[j] >= 0)
-          *reinterpret_cast<bf16x8_t *>(g_tok_lds + dst[j]) = stage_vec<F16>(q1, xv[j], rg1);
+      if (units == 0)  // rows of an odd number of 4-byte scales or of single bytes
+        for (int i = tid; i < 2 * MT * kTile * a.rsc.n; i += kNT) {
+          const int r = (int)a.rsc.per1.div((uint32_t)i), o = i - r * a.rsc.n;
+          size_t row;
+          if (item_row(it, r, row))
+            scl[r * a.rsc.stride + o] = (char)sbase[row * a.rsc.n + o];
+        }
     }
-    __syncthreads();
-
-    // ---- this wave's chunks of the contraction, two batches of loads in turn
-    f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    const char *xs = g_tok_lds + min(col, nc - 1) * xstride + kq * kSeg * 2;
-    auto compute = [&](Raw (&r)[kU][2], int cb) {
-      f32x4 cs[kU][2];
-      if (MODE == kPost) {
+    if (kZp)
+      for (int i = tid; i < 2 * MT * kTile * a.rzp.n; i += kNT) {
+        const int r = (int)a.rzp.per1.div((uint32_t)i), o = i - r * a.rzp.n;
+        size_t row;
+        if (item_row(it, r, row)) zpl[r * a.rzp.stride + o] = (char)w.zp[row * a.rzp.n + o];
+      }
+  };
+  // one segment's scales from LDS (r: the row in the item)
+  auto scales = [&](int r, int ch) {
+    Scales q;
+    const int k0 = ch * kChunk + kq * kSeg;
+    if (kSb) {
+      const char *p = scl + r * a.rsc.stride + ch * 8 + kq * 2;
+      if (WHOLE) {
+        q.sb = *reinterpret_cast<const uint16_t *>(p);
+      } else {
+        q.sb = k0 < w.K ? (uint32_t)(uint8_t)p[0] : 0u;
+        if (k0 + 16 < w.K) q.sb |= (uint32_t)(uint8_t)p[1] << 8;
+      }
+    }
+    if (kZp || (kS && MODE == kPre)) {
+      const int gi = (int)w.dgroup.div((uint32_t)min(k0, w.K - 1));
+      if (kS && MODE == kPre) q.s0 = *reinterpret_cast<const float *>(scl + r * a.rsc.stride + gi * 4);
+      if (kZp) q.zp = (float)(uint8_t)zpl[r * a.rzp.stride + gi];
+    }
+    return q;
+  };
+  auto chunk_scales = [&](int r, int ch) {  // kPost: of the four rows of a result that a lane holds
+    const int gi = (int)w.dgroup.div((uint32_t)(ch * kChunk));
+    f32x4 s;
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
-          if (cb + u * kWK < nch) {
-            cs[u][0] = chunk_scales<FMT>(w, row_g + 4 * kq, cb + u * kWK);
-            cs[u][1] = chunk_scales<FMT>(w, row_u + 4 * kq, cb + u * kWK);
+    for (int i = 0; i < 4; ++i)
+      s[i] = *reinterpret_cast<const float *>(scl + (r + 4 * kq + i) * a.rsc.stride + gi * 4);
+    return s;
+  };
+
+  point(it0);
+  int cur = -1, staged = -1;  // the listed expert, the column group in LDS
+  bool first = true;          // the first batch of weights is still to be requested
+  for (int it = it0; it < it1; ++it) {
+    const int sl = (int)a.dny.div((uint32_t)it), y = it - sl * a.ny;
+    const int e = __builtin_amdgcn_readfirstlane(plan.act[sl]);
+    const int n = __builtin_amdgcn_readfirstlane(plan.cnt[e]);
+    const int off = __builtin_amdgcn_readfirstlane(plan.off[e]);
+    if (sl != cur) {
+      list_rows(a, plan, ids, e, y == 0);
+      if (y == 0 && tid < n) {
+        a.tok[off + tid] = plan.tok[tid];
+        a.pw[off + tid] = plan.pw[tid];
+      }
+      cur = sl;
+      staged = -1;
+    }
+    // the factors of the channels that this thread finishes
+    float rs[kOut][2];
+#pragma unroll
+    for (int j = 0; j < kOut; ++j) {
+      const int i = tid + j * kNT, f = (y * MT + (i >> 8)) * kTile + (i & 15);
+      const bool in = i < MT * 256 && f < a.F;
+      rs[j][0] = in ? row_scale<FMT, MODE>(w, e, (size_t)e * w.N + f) : 0.0f;
+      rs[j][1] = in ? row_scale<FMT, MODE>(w, e, (size_t)e * w.N + a.F + f) : 0.0f;
+    }
+    for (int c0 = 0; c0 < n; c0 += a.ncol) {
+      const int nc = min(a.ncol, n - c0), nvec = nc * vpr;
+      // ---- the tokens' grid values into LDS, a row's vectors beyond K zero
+      // (vpr is even: both lanes of a 16-block take part together)
+      if (staged != c0) {
+        for (int i0 = 0; i0 < nvec; i0 += kX * kNT) {
+          bf16x8_t xv[kX];
+          int dst[kX];
+#pragma unroll
+          for (int j = 0; j < kX; ++j) {
+            const int i = i0 + j * kNT + tid;
+            const int c = (int)a.dvpr.div((uint32_t)i), v = i - c * vpr;
+            dst[j] = i < nvec ? c * xstride + v * 16 : -1;
+            xv[j] = {{0u, 0u, 0u, 0u}};
+            if (i < nvec && v < live)
+              xv[j] = reinterpret_cast<const bf16x8_t *>(a.x + (size_t)plan.tok[c0 + c] * w.K)[v];
           }
-      }
+          if (first) load(raw[0], wk * kU);
+          first = false;
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int ch = cb + u * kWK;
-        if (ch >= nch) break;
-        f32x4 s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
-        if (MODE != kPost) {
-          s0 = acc[0];
-          s1 = acc[1];
+          for (int j = 0; j < kX; ++j)
+            if (dst[j] >= 0)
+              *reinterpret_cast<bf16x8_t *>(xrows + dst[j]) = stage_vec<F16>(q1, xv[j], rg1);
         }
-#pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
-          const bf16x8_t b =
-              *reinterpret_cast<const bf16x8_t *>(xs + (ch * kChunk + st * 8) * 2);
-          s0 = mfma_step<FMT, MODE, F16>(r[u][0], st, b, s0);
-          s1 = mfma_step<FMT, MODE, F16>(r[u][1], st, b, s1);
-        }
-        if (MODE == kPost) {
-          acc[0] += s0 * cs[u][0];
-          acc[1] += s1 * cs[u][1];
-        } else {
-          acc[0] = s0;
-          acc[1] = s1;
-        }
+        staged = c0;
       }
-    };
-    for (int cb = wk; cb < nch; cb += 2 * kU * kWK) {
-      load(raw[1], cb + kU * kWK);
-      compute(raw[0], cb);
-      load(raw[0], cb + 2 * kU * kWK);
-      compute(raw[1], cb + kU * kWK);
-    }
-    __syncthreads();  // the staged rows are read: their space takes the sums
+      if (first) load(raw[0], wk * kU);
+      first = false;
+      if (c0 == 0) store_scales(it);
+      __syncthreads();
 
-    // ---- the shares' sums, SwiGLU, FQ_a2. Each wave holds its group's tiles.
-    f32x4 *red = reinterpret_cast<f32x4 *>(g_tok_lds);
-    red[(wave * 2 + 0) * 64 + lane] = acc[0];
-    red[(wave * 2 + 1) * 64 + lane] = acc[1];
-    __syncthreads();
-    // channel f of column c: 16 consecutive lanes hold a group's 16 channels
-    for (int i = tid; i < MT * 256; i += kNT) {
-      const int m = i >> 8, f = i & 15, c = (i >> 4) & 15;
-      const int fb = (blockIdx.y * MT + m) * kTile;
-      const int idx = ((f >> 2) * 16 + c) * 4 + (f & 3);
-      const float *rf = reinterpret_cast<const float *>(g_tok_lds) + m * kWK * 512;
-      float hg = 0.0f, hu = 0.0f;
+      // ---- this wave's chunks of the contraction, two batches of loads in turn
+      f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+      const char *xs = xrows + min(col, nc - 1) * xstride + kq * kSeg * 2;
+      const int rg = wm * kTile, ru = (MT + wm) * kTile;
+      auto compute = [&](Codes (&r)[kU][2], int cb) {
 #pragma unroll
-      for (int k = 0; k < kWK; ++k) {
-        hg += rf[k * 512 + idx];
-        hu += rf[k * 512 + 256 + idx];
-      }
-      if (fb >= a.F) continue;  // whole groups of 16 lanes
-      const size_t row = (size_t)e * w.N + fb + f;
-      hg = hg * row_scale<FMT, MODE>(w, e, row) * q1.s;
-      hu = hu * row_scale<FMT, MODE>(w, e, row + a.F) * q1.s;
-      float av[2] = {hg * sigmoid_hw(hg) * hu, 0.0f};
-      float theta = 0.0f;
-      if (q2.fmt == FQ_FMT_NVFP4) {
-        float amax = fabsf(av[0]);
+        for (int u = 0; u < kU; ++u) {
+          const int ch = cb + u;
+          if (ch >= nch) break;
+          const Scales qg = scales(rg + col, ch), qu = scales(ru + col, ch);
+          f32x4 s0 = {0, 0, 0, 0}, s1 = {0, 0, 0, 0};
+          if (MODE != kPost) {
+            s0 = acc[0];
+            s1 = acc[1];
+          }
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o, 64));
-        theta = block_theta(amax, 1.0f / (6.0f * q2.s));
+          for (int st = 0; st < kSteps; ++st) {
+            const bf16x8_t b =
+                *reinterpret_cast<const bf16x8_t *>(xs + (ch * kChunk + st * 8) * 2);
+            s0 = mfma_step<FMT, MODE, F16>(r[u][0], qg, st, b, s0);
+            s1 = mfma_step<FMT, MODE, F16>(r[u][1], qu, st, b, s1);
+          }
+          if (MODE == kPost) {
+            acc[0] += s0 * chunk_scales(rg, ch);
+            acc[1] += s1 * chunk_scales(ru, ch);
+          } else {
+            acc[0] = s0;
+            acc[1] = s1;
+          }
+        }
+      };
+      for (int cb = wk * kU; cb < nch; cb += 2 * kU * kWK) {
+        load(raw[1], cb + kU * kWK);
+        compute(raw[0], cb);
+        load(raw[0], cb + 2 * kU * kWK);
+        compute(raw[1], cb + kU * kWK);
       }
-      act_grid<2>(q2, theta, av);
-      const uint32_t v =
-          a.d.f16 ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(av[0], 0.0f))
-                  : f32_to_bf16(av[0]);
-      if (c < nc) a.a[(size_t)(off + c0 + c) * a.F + fb + f] = (uint16_t)v;
+      // the next pass's first weights: this item's next columns, or the next item
+      const bool more_c = c0 + a.ncol < n;
+      if (!more_c && it + 1 < it1) point(it + 1);
+      if (more_c || it + 1 < it1) load(raw[0], wk * kU);
+
+      // ---- the shares' sums, SwiGLU, FQ_a2. Each wave holds its group's tiles.
+      red[(wave * 2 + 0) * 64 + lane] = acc[0];
+      red[(wave * 2 + 1) * 64 + lane] = acc[1];
+      __syncthreads();
+      // channel f of column c: 16 consecutive lanes hold a group's 16 channels
+#pragma unroll
+      for (int j = 0; j < kOut; ++j) {
+        const int i = tid + j * kNT;
+        const int m = i >> 8, f = i & 15, c = (i >> 4) & 15;
+        const int g = y * MT + m;  // past F: the zero tail of A's row
+        if (i >= MT * 256 || g >= a.agroups) continue;  // whole groups of 16 lanes
+        const int idx = ((f >> 2) * 16 + c) * 4 + (f & 3);
+        const float *rf = reinterpret_cast<const float *>(red) + m * kWK * 512;
+        float hg = 0.0f, hu = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWK; ++k) {
+          hg += rf[k * 512 + idx];
+          hu += rf[k * 512 + 256 + idx];
+        }
+        hg = hg * rs[j][0] * q1.s;
+        hu = hu * rs[j][1] * q1.s;
+        float av[2] = {hg * sigmoid_hw(hg) * hu, 0.0f};
+        float theta = 0.0f;
+        if (q2.fmt == FQ_FMT_NVFP4) {
+          float amax = fabsf(av[0]);
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o, 64));
+          theta = block_theta(amax, rg2);
+        }
+        act_grid<2>(q2, theta, av);
+        uint32_t v = a.d.f16 ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(av[0], 0.0f))
+                             : f32_to_bf16(av[0]);
+        if (g * kTile >= a.F) v = 0u;
+        if (c < nc)
+          a.a[(size_t)(off + c0 + c) * a.arow + a_index(a.d.seg, g * kTile + f)] = (uint16_t)v;
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -569,115 +725,181 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
 // once either way). A wave takes units (two experts, part of the contraction)
 // in turn and adds their weighted sums to its own [T, 8] block in LDS; the
 // waves' blocks are added in wave order.
-template <int FMT, int MODE, bool F16>
+template <int FMT, int MODE, bool F16, bool WHOLE>
 __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
   constexpr int kChunk = Fmt<FMT>::kChunk, kSeg = Fmt<FMT>::kSeg, kSteps = Fmt<FMT>::kSteps;
-  constexpr int kU = FMT == FQ_FMT_NONE ? 6 : Fmt<FMT>::k4bit ? 3 : 4;
-  __shared__ int32_t act_e[1024];
-  __shared__ int2 act_span[1024];
-  __shared__ int wcnt[kWavesD];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  constexpr bool kSb = Has<FMT, MODE>::kSb, kS = Has<FMT, MODE>::kS, kZp = Has<FMT, MODE>::kZp;
+  constexpr int kU = Fmt<FMT>::k4bit ? 2 : 4;  // chunks of a batch
+  __shared__ int4 act[1024];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n0 = blockIdx.x * 8;
-  float *accs = reinterpret_cast<float *>(g_tok_lds);  // [wave][T][8]
-
-  // the slots with work, in slot order (there are at most as many as threads)
-  const int2 sp = tid < a.slots ? a.span[tid] : make_int2(0, 0);
-  const int my_e = sp.y > 0 ? slot_expert(a, tid) : 0;
-  for (int i = tid; i < kWavesD * a.T * 8; i += kNTd) accs[i] = 0.0f;
-  const uint64_t m = __ballot(sp.y > 0);
-  if (lane == 0) wcnt[wave] = __popcll(m);
-  __syncthreads();
-  int base = 0, na = 0;
-  for (int w = 0; w < kWavesD; ++w) {
-    if (w < wave) base += wcnt[w];
-    na += wcnt[w];
-  }
-  if (sp.y > 0) {
-    const int i = base + __popcll(m & ((1ull << lane) - 1ull));
-    act_e[i] = my_e;
-    act_span[i] = sp;
-  }
-  __syncthreads();
-
   const TokStack &w = a.d;
   const ActQ q2 = load_actq(a.afmt2, a.as2);
+  float *accs = reinterpret_cast<float *>(g_tok_lds);  // [wave][T][8]
+  const int na = a.nact[0];
+  if (tid < min(a.P, a.E)) act[tid] = a.act[tid];  // behind na: stale, not used
+  for (int i = tid; i < kWavesD * a.T * 8; i += kNTd) accs[i] = 0.0f;
+  __syncthreads();
+
   const int nch = w.nch;
   const int col = lane & 15, kq = lane >> 4;
   const int pairs = (na + 1) / 2;
-  // parts of a contraction, so that few experts still occupy every wave
+  // parts of a contraction (whole batches), so that few experts still occupy
+  // every wave
   int kp = pairs > 0 ? kWavesD / pairs : 1;
-  kp = max(1, min(kp, nch));
-  const int per = (nch + kp - 1) / kp;
-  for (int u = wave; u < pairs * kp; u += kWavesD) {
-    const int pr = u / kp, part = u - pr * kp;
-    const int ch0 = part * per, ch1 = min(nch, ch0 + per);
-    // this lane's weight row, its column's row of A, and the rows and column
-    // of the result it holds
-    // (without a second expert its lanes repeat the first: their part of the
-    // result is not used)
-    const int i1 = min(2 * pr + 1, na - 1);
-    const int iw = (col >> 3) ? i1 : 2 * pr, ir = (kq >> 1) ? i1 : 2 * pr;
-    const bool has_w = 2 * pr + (col >> 3) < na;
-    const int2 sc = act_span[iw];
-    const RowPtr pw = row_ptr<FMT, MODE>(w, (size_t)act_e[iw] * w.N + n0 + (col & 7), kq);
-    const int er = act_e[ir];
-    const size_t row_r = (size_t)er * w.N + n0 + 4 * (kq & 1);
-    const int nmax = max(act_span[2 * pr].y, act_span[i1].y);
-    for (int c0 = 0; c0 < nmax; c0 += 8) {
-      // a column past the expert's last repeats it, and is not used
-      const bool live_c = has_w && c0 + (col & 7) < sc.y;
-      const int r = sc.x + min(c0 + (col & 7), sc.y - 1);
-      const uint16_t *ap = a.a + (size_t)r * a.F + kq * kSeg;
-      const int t = a.tok[r];
-      const float p = a.pw[r];
-      f32x4 acc = {0, 0, 0, 0};
-      for (int cb = ch0; cb < ch1; cb += kU) {
-        Raw raw[kU];
-        f32x4 cs[kU];
-        bf16x8_t b[kU][kSteps];
+  kp = max(1, min(kp, (nch + kU - 1) / kU));
+  const int per = ((nch + kp - 1) / kp + kU - 1) / kU * kU;
+
+  // Where a wave stands: unit u (two experts, a part of the contraction), the
+  // batch of chunks from cb on, the columns from c0 on. Without a second expert
+  // its lanes repeat the first: their part of the result is not used.
+  struct At {
+    int u, cb, ch0, ch1, c0, nmax, i0, i1;
+    size_t row;        // the lane's weight row
+    const uint8_t *p;  // its codes
+  };
+  auto enter = [&](At &t) {
+    if (t.u >= pairs * kp) return;
+    const int pr = t.u / kp, part = t.u - pr * kp;
+    t.ch0 = t.cb = part * per;
+    t.ch1 = min(nch, t.ch0 + per);
+    t.c0 = 0;
+    t.i0 = 2 * pr;
+    t.i1 = min(2 * pr + 1, na - 1);
+    t.nmax = max(__builtin_amdgcn_readfirstlane(act[t.i0].z),
+                 __builtin_amdgcn_readfirstlane(act[t.i1].z));
+    t.row = (size_t)act[(col >> 3) ? t.i1 : t.i0].x * w.N + n0 + (col & 7);
+    t.p = row_codes<FMT>(w, t.row, kq);
+  };
+  struct Batch {
+    Codes c[kU];
+    uint2 sb[kU];  // NVFP4: the chunk's eight block scale bytes of the lane's row
+    float s[kU];   // kS: the segment's scale (kPost: the chunk's)
+    uint8_t zp[kU];
+  };
+  auto load = [&](Batch &r, const At &t) {
+    const uint8_t *ps = w.sbytes + t.row * (size_t)(w.K >> 4) + t.cb * 8;
+    // rows of whole pairs of chunks: both chunks' scale bytes in one load
+    const bool wide = WHOLE && kSb && kU == 2 && (w.K & 255) == 0;
+    if (wide && t.cb < t.ch1) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(ps);
+      r.sb[0] = make_uint2(v.x, v.y);
+      r.sb[1] = make_uint2(v.z, v.w);
+    }
 #pragma unroll
-        for (int i = 0; i < kU; ++i)
-          if (cb + i < ch1) {
-            raw[i] = load_raw<FMT, MODE>(w, pw, cb + i, kq);
-#pragma unroll
-            for (int st = 0; st < kSteps; ++st) {
-              const int k = (cb + i) * kChunk + st * 8;
-              if (w.whole) {
-                b[i][st] = *reinterpret_cast<const bf16x8_t *>(ap + k);
-              } else {
-                b[i][st] = {{0u, 0u, 0u, 0u}};
-                if (k + kq * kSeg < w.K)
-                  b[i][st] = *reinterpret_cast<const bf16x8_t *>(ap + k);
-              }
-            }
-            if (MODE == kPost) cs[i] = chunk_scales<FMT>(w, row_r, cb + i);
+    for (int i = 0; i < kU; ++i)
+      if (t.cb + i < t.ch1) {
+        r.c[i] = load_codes<FMT, WHOLE>(w, t.p, t.cb + i, kq);
+        if (kSb && !wide) {
+          if (WHOLE) {
+            r.sb[i] = *reinterpret_cast<const uint2 *>(ps + i * 8);
+          } else {
+            const int k0 = (t.cb + i) * kChunk + kq * kSeg;
+            const uint8_t *b = ps + i * 8 + kq * 2;
+            uint32_t v = k0 < w.K ? (uint32_t)b[0] : 0u;
+            if (k0 + 16 < w.K) v |= (uint32_t)b[1] << 8;
+            v <<= (kq & 1) * 16;  // where the others have it
+            r.sb[i] = make_uint2(v, v);
           }
-#pragma unroll
-        for (int i = 0; i < kU; ++i) {
-          if (cb + i >= ch1) break;
-          f32x4 s = {0, 0, 0, 0};
-          if (MODE != kPost) s = acc;
-#pragma unroll
-          for (int st = 0; st < kSteps; ++st) s = mfma_step<FMT, MODE, F16>(raw[i], st, b[i][st], s);
-          if (MODE == kPost) acc += s * cs[i];
-          else acc = s;
+        }
+        if (kS || kZp) {
+          const int k0 = (t.cb + i) * kChunk + (MODE == kPost ? 0 : kq * kSeg);
+          const size_t gi = t.row * w.groups + w.dgroup.div((uint32_t)min(k0, w.K - 1));
+          if (kS) r.s[i] = w.scale[gi];
+          if (kZp) r.zp[i] = w.zp[gi];
         }
       }
-      const float ps = p * q2.s;
+  };
+
+  f32x4 acc = {0, 0, 0, 0};
+  f32x4 rs = {1, 1, 1, 1};  // factors of the four rows of the result a lane holds
+  int tok = 0;              // its column's token and weight
+  float p = 0.0f;
+  // One batch: its activation rows are requested first, then the next batch's
+  // weights, which are on their way while this one computes.
+  auto step = [&](Batch &r, Batch &rn, At &t) {
+    const int4 ac = act[(col >> 3) ? t.i1 : t.i0], ar = act[(kq >> 1) ? t.i1 : t.i0];
+    // a column past the expert's last repeats it, and is not used
+    const int row_a = ac.y + min(t.c0 + (col & 7), ac.z - 1);
+    if (t.cb == t.ch0) {
+      const size_t row_r = (size_t)ar.x * w.N + n0 + 4 * (kq & 1);
+      acc = {0, 0, 0, 0};
+      tok = a.tok[row_a];
+      p = a.pw[row_a];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = acc[i] * row_scale<FMT, MODE>(w, er, row_r + i) * ps;
+      for (int i = 0; i < 4; ++i) rs[i] = row_scale<FMT, MODE>(w, ar.x, row_r + i);
+    }
+    const uint16_t *ap = a.a + (size_t)row_a * a.arow + t.cb * kChunk + kq * 8;
+    bf16x8_t b[kU][kSteps];
+#pragma unroll
+    for (int i = 0; i < kU; ++i)
+      if (t.cb + i < t.ch1) {
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st)
+          b[i][st] = *reinterpret_cast<const bf16x8_t *>(ap + i * kChunk + st * 32);
+      }
+    At nx = t;
+    nx.cb += kU;
+    if (nx.cb >= nx.ch1) {
+      nx.cb = nx.ch0;
+      nx.c0 += 8;
+      if (nx.c0 >= nx.nmax) {
+        nx.u += kWavesD;
+        enter(nx);
+      }
+    }
+    if (nx.u < pairs * kp) load(rn, nx);
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      if (t.cb + i >= t.ch1) break;
+      Scales q;
+      if (kSb) q.sb = (((kq >> 1) ? r.sb[i].y : r.sb[i].x) >> ((kq & 1) * 16)) & 0xFFFFu;
+      if (kS) q.s0 = r.s[i];
+      if (kZp) q.zp = (float)r.zp[i];
+      f32x4 s = {0, 0, 0, 0};
+      if (MODE != kPost) s = acc;
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) s = mfma_step<FMT, MODE, F16>(r.c[i], q, st, b[i][st], s);
+      if (MODE == kPost) {
+        // weight row 4 kq + i of the result is lane 4 kq + i's row
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] += s[j] * __shfl(r.s[i], 4 * kq + j, 64);
+      } else {
+        acc = s;
+      }
+    }
+    if (t.cb + kU >= t.ch1) {  // these columns' sums are complete
+      const bool live_c = 2 * (t.u / kp) + (col >> 3) < na && t.c0 + (col & 7) < ac.z;
+      const float ps = p * q2.s;
+      const f32x4 v = acc * rs * ps;
       // a token may be in both experts' columns: one expert's lanes after the
       // other's (a wave's LDS accesses execute in order)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (live_c && (col >> 3) == h && (kq >> 1) == h) {
           f32x4 *dst =
-              reinterpret_cast<f32x4 *>(accs + ((size_t)wave * a.T + t) * 8 + 4 * (kq & 1));
-          *dst += acc;
+              reinterpret_cast<f32x4 *>(accs + ((size_t)wave * a.T + tok) * 8 + 4 * (kq & 1));
+          *dst += v;
         }
         __builtin_amdgcn_wave_barrier();
         asm volatile("" ::: "memory");
       }
+    }
+    t = nx;
+  };
+
+  At t;
+  t.u = wave;
+  if (t.u < pairs * kp) {
+    Batch r0, r1;
+    enter(t);
+    load(r0, t);
+    while (true) {
+      step(r0, r1, t);
+      if (t.u >= pairs * kp) break;
+      step(r1, r0, t);
+      if (t.u >= pairs * kp) break;
     }
   }
   __syncthreads();
@@ -709,6 +931,7 @@ TokStack tok_stack(const fq_stored_w &w, int N, int K, int afmt) {
   t.groups = w.group > 0 ? K / w.group : 0;
   t.nch = (K + chunk - 1) / chunk;
   t.whole = K % chunk == 0;
+  t.seg = chunk / 4;
   t.f16 = w.fmt == FQ_FMT_NVFP4 && afmt != FQ_FMT_NONE;
   t.dgroup = FastDiv((uint32_t)group);
   return t;
@@ -723,14 +946,23 @@ struct Launch {
 
 template <int FMT, int MODE, bool F16>
 void launch_one(const Launch &l, const TokArgs &a, hipStream_t st) {
-  if (l.down)
-    hipLaunchKernelGGL((k_tok_down<FMT, MODE, F16>), l.grid, dim3(kNTd), l.lds, st, a);
-  else if (l.mt == 4)
-    hipLaunchKernelGGL((k_tok_gate_up<FMT, MODE, F16, 4>), l.grid, dim3(kNT), l.lds, st, a);
-  else if (l.mt == 2)
-    hipLaunchKernelGGL((k_tok_gate_up<FMT, MODE, F16, 2>), l.grid, dim3(kNT), l.lds, st, a);
-  else
-    hipLaunchKernelGGL((k_tok_gate_up<FMT, MODE, F16, 1>), l.grid, dim3(kNT), l.lds, st, a);
+#define FQ_GU(WHOLE, MT)                                                                        \
+  hipLaunchKernelGGL((k_tok_gate_up<FMT, MODE, F16, WHOLE, MT>), l.grid, dim3(kNT), l.lds, st, a)
+  if (l.down) {
+    if (a.d.whole)
+      hipLaunchKernelGGL((k_tok_down<FMT, MODE, F16, true>), l.grid, dim3(kNTd), l.lds, st, a);
+    else
+      hipLaunchKernelGGL((k_tok_down<FMT, MODE, F16, false>), l.grid, dim3(kNTd), l.lds, st, a);
+  } else if (!a.gu.whole) {  // (two channel groups: see launch_moe_tokens)
+    FQ_GU(false, 2);
+  } else if (l.mt == 4) {
+    FQ_GU(true, 4);
+  } else if (l.mt == 2) {
+    FQ_GU(true, 2);
+  } else {
+    FQ_GU(true, 1);
+  }
+#undef FQ_GU
 }
 
 template <int FMT>
@@ -757,14 +989,16 @@ void launch_fmt(const fq_stored_w &w, const Launch &l, const TokArgs &a, hipStre
 inline size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 struct TokWs {
-  size_t a, span, tok, pw, total;
+  size_t a, act, nact, tok, pw, total;
 };
 TokWs tok_ws(int T, int topk, int E, int F) {
+  const int arow = (F + 127) / 128 * 128;  // whole chunks in every format
   const size_t P = (size_t)T * topk, slots = P < (size_t)E ? P : (size_t)E;
   TokWs w;
   size_t o = 0;
-  w.a = o;     o += up256(P * F * 2);
-  w.span = o;  o += up256(slots * 8);
+  w.a = o;     o += up256(P * arow * 2);
+  w.act = o;   o += up256(slots * 16);
+  w.nact = o;  o += 256;
   w.tok = o;   o += up256(P * 4);
   w.pw = o;    o += up256(P * 4);
   w.total = o;
@@ -792,7 +1026,6 @@ void launch_moe_tokens(const uint16_t *x, int T, int H, int F, const int32_t *id
   a.P = T * topk;
   a.ebegin = ebegin;
   a.E = E;
-  a.slots = a.P < E ? a.P : E;
   a.dtopk = FastDiv((uint32_t)topk);
   a.afmt1 = afmt1;
   a.afmt2 = afmt2;
@@ -803,24 +1036,42 @@ void launch_moe_tokens(const uint16_t *x, int T, int H, int F, const int32_t *id
   a.H = H;
   a.F = F;
   a.a = reinterpret_cast<uint16_t *>(b + o.a);
-  a.span = reinterpret_cast<int2 *>(b + o.span);
+  a.act = reinterpret_cast<int4 *>(b + o.act);
+  a.nact = reinterpret_cast<int32_t *>(b + o.nact);
   a.tok = reinterpret_cast<int32_t *>(b + o.tok);
   a.pw = reinterpret_cast<float *>(b + o.pw);
   a.out = out;
-  // token rows staged at a time: 16 columns of an MFMA, or what 40 KB hold
-  // (three blocks to a CU), at least one
+  // token rows staged at a time: 16 columns of an MFMA, or what 34 KB hold
+  // (two blocks to a CU beside the sums and scales), at least one
   const int chunk = chunk_of(w_gu.fmt), row = xrow_bytes(H, chunk);
-  int nc = (40 << 10) / row;
+  int nc = (34 << 10) / row;
   nc = nc < 1 ? 1 : nc > 16 ? 16 : nc;
   a.ncol = nc < T ? nc : T;
   a.dvpr = FastDiv((uint32_t)(a.gu.nch * (chunk / 8)));
-  // channel groups per gate_up block: the most that leave four blocks to a CU
-  const int groups = F / kTile;
+  a.idb = (a.P * 2 + 15) / 16 * 16;
+  a.xb = a.ncol * row;
+  // channel groups per gate_up item: the most that leave two items to a block.
+  // A's zero tail up to whole chunks of the down projection counts as channels.
+  a.arow = a.d.nch * a.d.seg * 4;
+  a.agroups = a.arow / kTile;
+  const int slots = a.P < E ? a.P : E;
   int mt = 4;
-  while (mt > 1 && (long)a.slots * ((groups + mt - 1) / mt) < 1024) mt /= 2;
-  int lds = a.ncol * row;
-  if (lds < kRedBytes) lds = kRedBytes;
-  launch_fmt(w_gu, {false, mt, dim3(a.slots, (groups + mt - 1) / mt), lds}, a, st);
+  while (mt > 1 && (long)slots * ((a.agroups + mt - 1) / mt) < 1024) mt /= 2;
+  // bytes of a row's scales, fewer channels to an item where they are many
+  const int f = w_gu.fmt, ng = a.gu.groups;
+  const bool grouped = f != FQ_FMT_NONE && f != FQ_FMT_NVFP4 && ng > 1;
+  a.rsc = row_bytes(f == FQ_FMT_NVFP4 ? H / 16 : grouped ? 4 * ng : 0);
+  a.rzp = row_bytes(f == FQ_FMT_INT4 ? ng : 0);
+  const int per_row = (a.rsc.n ? a.rsc.stride : 0) + (a.rzp.n ? a.rzp.stride : 0);
+  while (mt > 1 && 2 * mt * kTile * per_row > (20 << 10)) mt /= 2;
+  if (!a.gu.whole) mt = 2;
+  a.ny = (a.agroups + mt - 1) / mt;
+  a.dny = FastDiv((uint32_t)a.ny);
+  // blocks: two to a CU, at most one per item
+  const long items = (long)slots * a.ny;
+  const int blocks = (int)(items < 512 ? items : 512);
+  launch_fmt(w_gu, {false, mt, dim3(blocks), a.idb + a.xb + kRedBytes + 2 * mt * kTile * per_row}, a,
+             st);
   launch_fmt(w_d, {true, 0, dim3(H / 8), kWavesD * T * 8 * 4}, a, st);
 }
 

@@ -83,8 +83,9 @@ def test_refusals(pkg):  # noqa: F811
                 dict(H=0), dict(F=-16), dict(topk=0), dict(E=0), dict(begin=-1),
                 dict(begin=2 ** 31 - 4), dict(x=P + 8), dict(out=P + 2), dict(a1=noscale),
                 dict(a2=noscale), dict(gu=w(fmt=9)), dict(gu=w(codes=None)), dict(d=w(codes=P + 8)),
-                dict(gu=w(group=32)), dict(gu=w(sb=None)), dict(d=w(g=None)), dict(d=w(sb=P + 1)),
-                dict(gu=w(pkg.FMT_INT8, 256, scale=None)), dict(gu=w(pkg.FMT_INT4, 128, zp=None)),
+                dict(gu=w(group=32)), dict(gu=w(sb=None)), dict(d=w(g=None)), dict(d=w(sb=P + 8)),
+                dict(gu=w(pkg.FMT_INT8, 256, scale=None)), dict(gu=w(pkg.FMT_INT8, 256, scale=P + 4)),
+                dict(gu=w(pkg.FMT_INT4, 128, zp=P + 1)), dict(gu=w(pkg.FMT_INT4, 128, zp=None)),
                 dict(gu=w(pkg.FMT_INT4, -1)), dict(gu=w(pkg.FMT_INT8, 96)),
                 dict(gu=w(pkg.FMT_FP8_E4M3, 24)), dict(gu=w(pkg.FMT_INT8, 0)), dict(ws=P + 8)):
         assert call(**bad) == arg, bad
@@ -114,4 +115,4 @@ def test_workspace_holds_every_buffer(pkg):  # noqa: F811
                 P = T * topk
                 slots = min(P, E)
                 got = pkg.fq_workspace_bytes(pkg.FQ_OP_MOE_TOKENS, (E, H, Fc), P, topk)
-                assert got >= P * Fc * 2 + slots * 8 + P * 8
+                assert got >= P * Fc * 2 + slots * 16 + P * 8
