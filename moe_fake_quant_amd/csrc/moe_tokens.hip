@@ -311,6 +311,14 @@ __host__ __device__ inline int xrow_bytes(int K, int chunk) {
 
 extern __shared__ __attribute__((aligned(16))) char g_tok_lds[];
 
+// v, but not known to be the same each time: index arithmetic made from it is
+// done again where it is used, instead of being kept in registers over the
+// contraction loop (which then spill).
+__device__ __forceinline__ int anew(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // The plan of a batch, made by every gate_up block for itself (it costs less
 // than waiting for another kernel): rows = the local pairs in expert order,
 // within an expert in pair order, a pair that repeats an expert of its token
@@ -523,10 +531,42 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
     return f < a.F;
   };
   const int units = a.rsc.n % 8 == 0 ? 2 * MT * kTile * (a.rsc.n / 8) : 0;
-  auto store_scales = [&](int it) {
+  constexpr int kPf = kSb || kS ? 4 : 1;  // units a thread requests ahead
+  uint2 pf[kPf];
+  float rsn[kOut][2];  // factors of the channels that this thread finishes, next item's
+  // what an item needs besides its codes, requested before them: loads return in order
+  auto request = [&](int it) {
+    const int tid = anew(threadIdx.x);
     if (kSb || kS) {
-#pragma unroll 2
-      for (int i = tid; i < units; i += kNT) {
+#pragma unroll
+      for (int j = 0; j < kPf; ++j) {
+        const int i = tid + j * kNT;
+        const int r = (int)a.rsc.per8.div((uint32_t)i), o = (i - r * (a.rsc.n / 8)) * 8;
+        size_t row;
+        if (i < units && item_row(it, r, row))
+          pf[j] = *reinterpret_cast<const uint2 *>(sbase + row * a.rsc.n + o);
+      }
+    }
+    const int sl = (int)a.dny.div((uint32_t)it), y = it - sl * a.ny;
+    const int e = __builtin_amdgcn_readfirstlane(plan.act[sl]);
+#pragma unroll
+    for (int j = 0; j < kOut; ++j) {
+      const int i = tid + j * kNT, f = (y * MT + (i >> 8)) * kTile + (i & 15);
+      const bool in = i < MT * 256 && f < a.F;
+      rsn[j][0] = in ? row_scale<FMT, MODE>(w, e, (size_t)e * w.N + f) : 0.0f;
+      rsn[j][1] = in ? row_scale<FMT, MODE>(w, e, (size_t)e * w.N + a.F + f) : 0.0f;
+    }
+  };
+  auto store_scales = [&](int it) {
+    const int tid = anew(threadIdx.x);
+    if (kSb || kS) {
+#pragma unroll
+      for (int j = 0; j < kPf; ++j) {
+        const int i = tid + j * kNT;
+        const int r = (int)a.rsc.per8.div((uint32_t)i), o = (i - r * (a.rsc.n / 8)) * 8;
+        if (i < units) *reinterpret_cast<uint2 *>(scl + r * a.rsc.stride + o) = pf[j];
+      }
+      for (int i = tid + kPf * kNT; i < units; i += kNT) {
         const int r = (int)a.rsc.per8.div((uint32_t)i), o = (i - r * (a.rsc.n / 8)) * 8;
         size_t row;
         if (item_row(it, r, row))
@@ -578,8 +618,9 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
   };
 
   point(it0);
+  request(it0);
+  load(raw[0], wk * kU);
   int cur = -1, staged = -1;  // the listed expert, the column group in LDS
-  bool first = true;          // the first batch of weights is still to be requested
   for (int it = it0; it < it1; ++it) {
     const int sl = (int)a.dny.div((uint32_t)it), y = it - sl * a.ny;
     const int e = __builtin_amdgcn_readfirstlane(plan.act[sl]);
@@ -594,20 +635,19 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
       cur = sl;
       staged = -1;
     }
-    // the factors of the channels that this thread finishes
     float rs[kOut][2];
 #pragma unroll
     for (int j = 0; j < kOut; ++j) {
-      const int i = tid + j * kNT, f = (y * MT + (i >> 8)) * kTile + (i & 15);
-      const bool in = i < MT * 256 && f < a.F;
-      rs[j][0] = in ? row_scale<FMT, MODE>(w, e, (size_t)e * w.N + f) : 0.0f;
-      rs[j][1] = in ? row_scale<FMT, MODE>(w, e, (size_t)e * w.N + a.F + f) : 0.0f;
+      rs[j][0] = rsn[j][0];
+      rs[j][1] = rsn[j][1];
     }
+    store_scales(it);
     for (int c0 = 0; c0 < n; c0 += a.ncol) {
       const int nc = min(a.ncol, n - c0), nvec = nc * vpr;
       // ---- the tokens' grid values into LDS, a row's vectors beyond K zero
       // (vpr is even: both lanes of a 16-block take part together)
       if (staged != c0) {
+        const int tid = anew(threadIdx.x);
         for (int i0 = 0; i0 < nvec; i0 += kX * kNT) {
           bf16x8_t xv[kX];
           int dst[kX];
@@ -620,8 +660,6 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
             if (i < nvec && v < live)
               xv[j] = reinterpret_cast<const bf16x8_t *>(a.x + (size_t)plan.tok[c0 + c] * w.K)[v];
           }
-          if (first) load(raw[0], wk * kU);
-          first = false;
 #pragma unroll
           for (int j = 0; j < kX; ++j)
             if (dst[j] >= 0)
@@ -629,9 +667,6 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
         }
         staged = c0;
       }
-      if (first) load(raw[0], wk * kU);
-      first = false;
-      if (c0 == 0) store_scales(it);
       __syncthreads();
 
       // ---- this wave's chunks of the contraction, two batches of loads in turn
@@ -673,7 +708,10 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
       }
       // the next pass's first weights: this item's next columns, or the next item
       const bool more_c = c0 + a.ncol < n;
-      if (!more_c && it + 1 < it1) point(it + 1);
+      if (!more_c && it + 1 < it1) {
+        point(it + 1);
+        request(it + 1);
+      }
       if (more_c || it + 1 < it1) load(raw[0], wk * kU);
 
       // ---- the shares' sums, SwiGLU, FQ_a2. Each wave holds its group's tiles.
@@ -681,9 +719,10 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
       red[(wave * 2 + 1) * 64 + lane] = acc[1];
       __syncthreads();
       // channel f of column c: 16 consecutive lanes hold a group's 16 channels
+      const int tid_e = anew(threadIdx.x);
 #pragma unroll
       for (int j = 0; j < kOut; ++j) {
-        const int i = tid + j * kNT;
+        const int i = tid_e + j * kNT;
         const int m = i >> 8, f = i & 15, c = (i >> 4) & 15;
         const int g = y * MT + m;  // past F: the zero tail of A's row
         if (i >= MT * 256 || g >= a.agroups) continue;  // whole groups of 16 lanes
