@@ -108,7 +108,7 @@ struct TokArgs {
   int ncol;                 // columns (tokens) staged at a time by the gate_up kernel
   int ny;                   // channel blocks of a gate_up expert
   FastDiv dny;
-  FastDiv dvpr;             // / 8-element vectors of a staged token row
+  FastDiv dvpr, dncol;      // / 8-element vectors of a staged token row, / ncol
   int idb, xb;              // gate_up LDS: bytes of the ids, of the staged rows
   RowBytes rsc, rzp;        // gate_up: scale (or scale byte) and zero point bytes of a row
   int agroups, arow;        // A's 16-channel groups and row length, padded to whole chunks
@@ -329,10 +329,12 @@ struct Plan {
   int cnt[1024];       // rows of an expert
   uint16_t off[1024];  // its first row
   uint16_t act[1024];  // the experts with rows, ascending
-  uint32_t wsum[kWaves];
+  uint16_t pass[1025]; // column passes (of ncol rows) of the experts before
+  uint32_t wsum[kWaves], psum[kWaves];
   int32_t tok[128];    // tokens of the current expert's rows
-  float pw[128];
+  int32_t pair[128];   // their pairs
   int wcnt[kWaves];
+  int it[2];
 };
 
 // ids: LDS, P entries: the pair's local expert | kRepeat. Returns the number of
@@ -358,38 +360,69 @@ __device__ __forceinline__ int make_plan(const TokArgs &a, Plan &p, uint16_t *id
   for (int q = tid, k = 0; q < a.P; q += kNT, ++k)
     if ((repeat >> k) & 1u) ids[q] |= kRepeat;
   // prefix sums over the experts, rows in the low half, experts with rows in the high
-  uint32_t run = 0;
+  uint32_t run = 0, prun = 0;
   for (int e0 = 0; e0 < a.E; e0 += kNT) {
     const int e = e0 + tid;
     const int c = e < a.E ? p.cnt[e] : 0;
     const uint32_t v = (uint32_t)c | (c > 0 ? 0x10000u : 0u);
-    uint32_t x = v;
+    const uint32_t u = a.dncol.div((uint32_t)(c + a.ncol - 1));
+    uint32_t x = v, z = u;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t y = __shfl_up(x, o, 64);
-      if (lane >= o) x += y;
+      const uint32_t xo = __shfl_up(x, o, 64), zo = __shfl_up(z, o, 64);
+      if (lane >= o) {
+        x += xo;
+        z += zo;
+      }
     }
-    if (lane == 63) p.wsum[wave] = x;
+    if (lane == 63) {
+      p.wsum[wave] = x;
+      p.psum[wave] = z;
+    }
     __syncthreads();
-    uint32_t base = run;
+    uint32_t base = run, pbase = prun;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      if (w < wave) base += p.wsum[w];
+      if (w < wave) {
+        base += p.wsum[w];
+        pbase += p.psum[w];
+      }
       run += p.wsum[w];
+      prun += p.psum[w];
     }
     if (c > 0) {
       const uint32_t ex = base + x - v;
       p.off[e] = (uint16_t)(ex & 0xFFFFu);
       p.act[ex >> 16] = (uint16_t)e;
+      p.pass[ex >> 16] = (uint16_t)(pbase + z - u);
     }
+    if (tid == 0) p.pass[run >> 16] = (uint16_t)prun;
     __syncthreads();
   }
   return (int)(run >> 16);
 }
 
-// The tokens (and, with_pw, the weights) of expert e's rows into p.tok / p.pw.
-__device__ __forceinline__ void list_rows(const TokArgs &a, Plan &p, const uint16_t *ids, int e,
-                                          bool with_pw) {
+// This block's items into p.it: those that begin in its share of the passes (an
+// expert's items count its passes each, so that a hot expert's weigh as much as
+// they take).
+__device__ __forceinline__ void my_items(const TokArgs &a, Plan &p, int na) {
+  const uint32_t total = (uint32_t)p.pass[na] * a.ny;
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t at = (uint32_t)((uint64_t)total * (blockIdx.x + h) / gridDim.x);
+    for (int sl = tid; sl < na; sl += kNT) {
+      const uint32_t b = p.pass[sl], e = p.pass[sl + 1];
+      if (at >= b * a.ny && at < e * a.ny)
+        p.it[h] = sl * a.ny + (int)((at - b * a.ny + (e - b) - 1) / (e - b));
+    }
+    if (tid == 0 && at == total) p.it[h] = na * a.ny;
+  }
+  __syncthreads();
+}
+
+// The tokens and pairs of expert e's rows.
+__device__ __forceinline__ void list_rows(const TokArgs &a, Plan &p, const uint16_t *ids, int e) {
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   int n = 0;
   for (int q0 = 0; q0 < a.P; q0 += kNT) {
@@ -406,14 +439,8 @@ __device__ __forceinline__ void list_rows(const TokArgs &a, Plan &p, const uint1
     }
     if (hit) {
       const int i = base + __popcll(m & ((1ull << lane) - 1ull));
-      const int t = (int)a.dtopk.div((uint32_t)q);
-      p.tok[i] = t;
-      if (with_pw) {
-        float v = a.probs[q];
-        for (int j = q + 1; j < (t + 1) * a.topk; ++j)
-          if (ids[j] == (uint16_t)(e | kRepeat)) v += a.probs[j];
-        p.pw[i] = v;
-      }
+      p.tok[i] = (int)a.dtopk.div((uint32_t)q);
+      p.pair[i] = q;
     }
     __syncthreads();
   }
@@ -471,9 +498,10 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
   __shared__ Plan plan;
   uint16_t *ids = reinterpret_cast<uint16_t *>(g_tok_lds);
   char *xrows = g_tok_lds + a.idb;
-  f32x4 *red = reinterpret_cast<f32x4 *>(g_tok_lds + a.idb + a.xb);
-  // scales and zero points of the item's rows: MT * 16 gate rows, then the up rows
-  char *scl = g_tok_lds + a.idb + a.xb + kRedBytes;
+  // scales and zero points of the item's rows (MT * 16 gate rows, then the up
+  // rows); the waves' sums take their space once they are used
+  char *scl = g_tok_lds + a.idb + a.xb;
+  f32x4 *red = reinterpret_cast<f32x4 *>(scl);
   char *zpl = scl + (kSb || kS ? 2 * MT * kTile * a.rsc.stride : 0);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform: scalar loop control
@@ -488,9 +516,10 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
       a.act[i] = make_int4(e, plan.off[e], plan.cnt[e], 0);
     }
   }
-  const uint32_t items = (uint32_t)(na * a.ny);
-  const int it0 = (int)((uint64_t)items * blockIdx.x / gridDim.x);
-  const int it1 = (int)((uint64_t)items * (blockIdx.x + 1) / gridDim.x);
+  if (na == 0) return;
+  my_items(a, plan, na);
+  const int it0 = __builtin_amdgcn_readfirstlane(plan.it[0]);
+  const int it1 = __builtin_amdgcn_readfirstlane(plan.it[1]);
   if (it0 >= it1) return;
 
   const float rg1 = 1.0f / (6.0f * q1.s), rg2 = 1.0f / (6.0f * q2.s);
@@ -557,16 +586,18 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
       rsn[j][1] = in ? row_scale<FMT, MODE>(w, e, (size_t)e * w.N + a.F + f) : 0.0f;
     }
   };
-  auto store_scales = [&](int it) {
+  auto store_scales = [&](int it, bool requested) {
     const int tid = anew(threadIdx.x);
     if (kSb || kS) {
+      if (requested) {
 #pragma unroll
-      for (int j = 0; j < kPf; ++j) {
-        const int i = tid + j * kNT;
-        const int r = (int)a.rsc.per8.div((uint32_t)i), o = (i - r * (a.rsc.n / 8)) * 8;
-        if (i < units) *reinterpret_cast<uint2 *>(scl + r * a.rsc.stride + o) = pf[j];
+        for (int j = 0; j < kPf; ++j) {
+          const int i = tid + j * kNT;
+          const int r = (int)a.rsc.per8.div((uint32_t)i), o = (i - r * (a.rsc.n / 8)) * 8;
+          if (i < units) *reinterpret_cast<uint2 *>(scl + r * a.rsc.stride + o) = pf[j];
+        }
       }
-      for (int i = tid + kPf * kNT; i < units; i += kNT) {
+      for (int i = tid + (requested ? kPf * kNT : 0); i < units; i += kNT) {
         const int r = (int)a.rsc.per8.div((uint32_t)i), o = (i - r * (a.rsc.n / 8)) * 8;
         size_t row;
         if (item_row(it, r, row))
@@ -627,11 +658,7 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
     const int n = __builtin_amdgcn_readfirstlane(plan.cnt[e]);
     const int off = __builtin_amdgcn_readfirstlane(plan.off[e]);
     if (sl != cur) {
-      list_rows(a, plan, ids, e, y == 0);
-      if (y == 0 && tid < n) {
-        a.tok[off + tid] = plan.tok[tid];
-        a.pw[off + tid] = plan.pw[tid];
-      }
+      list_rows(a, plan, ids, e);
       cur = sl;
       staged = -1;
     }
@@ -641,8 +668,8 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
       rs[j][0] = rsn[j][0];
       rs[j][1] = rsn[j][1];
     }
-    store_scales(it);
     for (int c0 = 0; c0 < n; c0 += a.ncol) {
+      store_scales(it, c0 == 0);
       const int nc = min(a.ncol, n - c0), nvec = nc * vpr;
       // ---- the tokens' grid values into LDS, a row's vectors beyond K zero
       // (vpr is even: both lanes of a 16-block take part together)
@@ -714,7 +741,16 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
       }
       if (more_c || it + 1 < it1) load(raw[0], wk * kU);
 
+      if (y == 0 && c0 == 0 && tid < n) {  // what the down kernel needs of this expert's rows
+        const int q = plan.pair[tid], t = plan.tok[tid];
+        float v = a.probs[q];
+        for (int j = q + 1; j < (t + 1) * a.topk; ++j)
+          if (ids[j] == (uint16_t)(e | kRepeat)) v += a.probs[j];
+        a.tok[off + tid] = t;
+        a.pw[off + tid] = v;
+      }
       // ---- the shares' sums, SwiGLU, FQ_a2. Each wave holds its group's tiles.
+      __syncthreads();
       red[(wave * 2 + 0) * 64 + lane] = acc[0];
       red[(wave * 2 + 1) * 64 + lane] = acc[1];
       __syncthreads();
@@ -768,7 +804,8 @@ template <int FMT, int MODE, bool F16, bool WHOLE>
 __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
   constexpr int kChunk = Fmt<FMT>::kChunk, kSeg = Fmt<FMT>::kSeg, kSteps = Fmt<FMT>::kSteps;
   constexpr bool kSb = Has<FMT, MODE>::kSb, kS = Has<FMT, MODE>::kS, kZp = Has<FMT, MODE>::kZp;
-  constexpr int kU = Fmt<FMT>::k4bit ? 2 : 4;  // chunks of a batch
+  constexpr int kU = 4;                        // chunks whose codes are requested together
+  constexpr int kB = Fmt<FMT>::k4bit ? 2 : 4;  // chunks whose activations are
   __shared__ int4 act[1024];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -784,11 +821,11 @@ __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
   const int nch = w.nch;
   const int col = lane & 15, kq = lane >> 4;
   const int pairs = (na + 1) / 2;
-  // parts of a contraction (whole batches), so that few experts still occupy
-  // every wave
+  // parts of a contraction (whole pairs of chunks), so that few experts still
+  // occupy every wave
   int kp = pairs > 0 ? kWavesD / pairs : 1;
-  kp = max(1, min(kp, (nch + kU - 1) / kU));
-  const int per = ((nch + kp - 1) / kp + kU - 1) / kU * kU;
+  kp = max(1, min(kp, (nch + 1) / 2));
+  const int per = ((nch + kp - 1) / kp + 1) / 2 * 2;
 
   // Where a wave stands: unit u (two experts, a part of the contraction), the
   // batch of chunks from cb on, the columns from c0 on. Without a second expert
@@ -820,11 +857,15 @@ __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
   auto load = [&](Batch &r, const At &t) {
     const uint8_t *ps = w.sbytes + t.row * (size_t)(w.K >> 4) + t.cb * 8;
     // rows of whole pairs of chunks: both chunks' scale bytes in one load
-    const bool wide = WHOLE && kSb && kU == 2 && (w.K & 255) == 0;
-    if (wide && t.cb < t.ch1) {
-      const uint4 v = *reinterpret_cast<const uint4 *>(ps);
-      r.sb[0] = make_uint2(v.x, v.y);
-      r.sb[1] = make_uint2(v.z, v.w);
+    const bool wide = WHOLE && kSb && (w.K & 255) == 0;
+    if (wide) {
+#pragma unroll
+      for (int i = 0; i < kU; i += 2)
+        if (t.cb + i < t.ch1) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(ps + i * 8);
+          r.sb[i] = make_uint2(v.x, v.y);
+          r.sb[i + 1] = make_uint2(v.z, v.w);
+        }
     }
 #pragma unroll
     for (int i = 0; i < kU; ++i)
@@ -870,14 +911,17 @@ __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
       for (int i = 0; i < 4; ++i) rs[i] = row_scale<FMT, MODE>(w, ar.x, row_r + i);
     }
     const uint16_t *ap = a.a + (size_t)row_a * a.arow + t.cb * kChunk + kq * 8;
-    bf16x8_t b[kU][kSteps];
+    bf16x8_t b[kB][kSteps];
+    auto load_b = [&](int i0) {
 #pragma unroll
-    for (int i = 0; i < kU; ++i)
-      if (t.cb + i < t.ch1) {
+      for (int i = 0; i < kB; ++i)
+        if (t.cb + i0 + i < t.ch1) {
 #pragma unroll
-        for (int st = 0; st < kSteps; ++st)
-          b[i][st] = *reinterpret_cast<const bf16x8_t *>(ap + i * kChunk + st * 32);
-      }
+          for (int st = 0; st < kSteps; ++st)
+            b[i][st] = *reinterpret_cast<const bf16x8_t *>(ap + (i0 + i) * kChunk + st * 32);
+        }
+    };
+    load_b(0);
     At nx = t;
     nx.cb += kU;
     if (nx.cb >= nx.ch1) {
@@ -892,6 +936,7 @@ __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       if (t.cb + i >= t.ch1) break;
+      if (i > 0 && i % kB == 0) load_b(i);
       Scales q;
       if (kSb) q.sb = (((kq >> 1) ? r.sb[i].y : r.sb[i].x) >> ((kq & 1) * 16)) & 0xFFFFu;
       if (kS) q.s0 = r.s[i];
@@ -899,7 +944,8 @@ __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
       f32x4 s = {0, 0, 0, 0};
       if (MODE != kPost) s = acc;
 #pragma unroll
-      for (int st = 0; st < kSteps; ++st) s = mfma_step<FMT, MODE, F16>(r.c[i], q, st, b[i][st], s);
+      for (int st = 0; st < kSteps; ++st)
+        s = mfma_step<FMT, MODE, F16>(r.c[i], q, st, b[i % kB][st], s);
       if (MODE == kPost) {
         // weight row 4 kq + i of the result is lane 4 kq + i's row
 #pragma unroll
@@ -1080,15 +1126,6 @@ void launch_moe_tokens(const uint16_t *x, int T, int H, int F, const int32_t *id
   a.tok = reinterpret_cast<int32_t *>(b + o.tok);
   a.pw = reinterpret_cast<float *>(b + o.pw);
   a.out = out;
-  // token rows staged at a time: 16 columns of an MFMA, or what 34 KB hold
-  // (two blocks to a CU beside the sums and scales), at least one
-  const int chunk = chunk_of(w_gu.fmt), row = xrow_bytes(H, chunk);
-  int nc = (34 << 10) / row;
-  nc = nc < 1 ? 1 : nc > 16 ? 16 : nc;
-  a.ncol = nc < T ? nc : T;
-  a.dvpr = FastDiv((uint32_t)(a.gu.nch * (chunk / 8)));
-  a.idb = (a.P * 2 + 15) / 16 * 16;
-  a.xb = a.ncol * row;
   // channel groups per gate_up item: the most that leave two items to a block.
   // A's zero tail up to whole chunks of the down projection counts as channels.
   a.arow = a.d.nch * a.d.seg * 4;
@@ -1106,11 +1143,22 @@ void launch_moe_tokens(const uint16_t *x, int T, int H, int F, const int32_t *id
   if (!a.gu.whole) mt = 2;
   a.ny = (a.agroups + mt - 1) / mt;
   a.dny = FastDiv((uint32_t)a.ny);
+  // token rows staged at a time: 16 columns of an MFMA, or what leaves two
+  // blocks to a CU (80 KB, 14 of them the plan), at least one
+  const int chunk = chunk_of(w_gu.fmt), row = xrow_bytes(H, chunk);
+  int sums = 2 * mt * kTile * per_row;
+  if (sums < kRedBytes) sums = kRedBytes;
+  a.idb = (a.P * 2 + 15) / 16 * 16;
+  int nc = ((80 << 10) - (14 << 10) - a.idb - sums) / row;
+  nc = nc < 1 ? 1 : nc > 16 ? 16 : nc;
+  a.ncol = nc < T ? nc : T;
+  a.xb = a.ncol * row;
+  a.dvpr = FastDiv((uint32_t)(a.gu.nch * (chunk / 8)));
+  a.dncol = FastDiv((uint32_t)a.ncol);
   // blocks: two to a CU, at most one per item
   const long items = (long)slots * a.ny;
   const int blocks = (int)(items < 512 ? items : 512);
-  launch_fmt(w_gu, {false, mt, dim3(blocks), a.idb + a.xb + kRedBytes + 2 * mt * kTile * per_row}, a,
-             st);
+  launch_fmt(w_gu, {false, mt, dim3(blocks), a.idb + a.xb + sums}, a, st);
   launch_fmt(w_d, {true, 0, dim3(H / 8), kWavesD * T * 8 * 4}, a, st);
 }
 
