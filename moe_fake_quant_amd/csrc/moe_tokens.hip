@@ -109,6 +109,7 @@ struct TokArgs {
   int ny;                   // channel blocks of a gate_up expert
   FastDiv dny;
   FastDiv dvpr, dncol;      // / 8-element vectors of a staged token row, / ncol
+  FastDiv dgrid;            // / blocks of the gate_up kernel
   int idb, xb;              // gate_up LDS: bytes of the ids, of the staged rows
   RowBytes rsc, rzp;        // gate_up: scale (or scale byte) and zero point bytes of a row
   int agroups, arow;        // A's 16-channel groups and row length, padded to whole chunks
@@ -311,6 +312,13 @@ __host__ __device__ inline int xrow_bytes(int K, int chunk) {
 
 extern __shared__ __attribute__((aligned(16))) char g_tok_lds[];
 
+// A barrier for data in LDS. (__syncthreads also waits for every global load in
+// flight, which would end each request made ahead of a barrier: measured 2-4 us
+// a barrier here.)
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // v, but not known to be the same each time: index arithmetic made from it is
 // done again where it is used, instead of being kept in registers over the
 // contraction loop (which then spill).
@@ -346,7 +354,7 @@ __device__ __forceinline__ int make_plan(const TokArgs &a, Plan &p, uint16_t *id
     ids[q] = id < (uint32_t)a.E ? (uint16_t)id : kNoId;
   }
   for (int e = tid; e < a.E; e += kNT) p.cnt[e] = 0;
-  __syncthreads();
+  lds_barrier();
   uint32_t repeat = 0;  // one bit per pair of this thread (P <= 128 * 64 = 16 kNT)
   for (int q = tid, k = 0; q < a.P; q += kNT, ++k) {
     const uint16_t id = ids[q];
@@ -356,7 +364,7 @@ __device__ __forceinline__ int make_plan(const TokArgs &a, Plan &p, uint16_t *id
     if (again) repeat |= 1u << k;
     else atomicAdd(&p.cnt[id], 1);
   }
-  __syncthreads();
+  lds_barrier();
   for (int q = tid, k = 0; q < a.P; q += kNT, ++k)
     if ((repeat >> k) & 1u) ids[q] |= kRepeat;
   // prefix sums over the experts, rows in the low half, experts with rows in the high
@@ -379,7 +387,7 @@ __device__ __forceinline__ int make_plan(const TokArgs &a, Plan &p, uint16_t *id
       p.wsum[wave] = x;
       p.psum[wave] = z;
     }
-    __syncthreads();
+    lds_barrier();
     uint32_t base = run, pbase = prun;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
@@ -397,7 +405,7 @@ __device__ __forceinline__ int make_plan(const TokArgs &a, Plan &p, uint16_t *id
       p.pass[ex >> 16] = (uint16_t)(pbase + z - u);
     }
     if (tid == 0) p.pass[run >> 16] = (uint16_t)prun;
-    __syncthreads();
+    lds_barrier();
   }
   return (int)(run >> 16);
 }
@@ -407,18 +415,19 @@ __device__ __forceinline__ int make_plan(const TokArgs &a, Plan &p, uint16_t *id
 // they take).
 __device__ __forceinline__ void my_items(const TokArgs &a, Plan &p, int na) {
   const uint32_t total = (uint32_t)p.pass[na] * a.ny;
+  const uint32_t share = a.dgrid.div(total), rest = total - share * gridDim.x;
   const int tid = threadIdx.x;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t at = (uint32_t)((uint64_t)total * (blockIdx.x + h) / gridDim.x);
+    const uint32_t b = blockIdx.x + h, at = b * share + min(b, rest);
     for (int sl = tid; sl < na; sl += kNT) {
-      const uint32_t b = p.pass[sl], e = p.pass[sl + 1];
-      if (at >= b * a.ny && at < e * a.ny)
-        p.it[h] = sl * a.ny + (int)((at - b * a.ny + (e - b) - 1) / (e - b));
+      const uint32_t p0 = p.pass[sl], n = p.pass[sl + 1] - p0;
+      if (at >= p0 * a.ny && at < (p0 + n) * a.ny)
+        p.it[h] = sl * a.ny + (int)((at - p0 * a.ny + n - 1) / n);
     }
     if (tid == 0 && at == total) p.it[h] = na * a.ny;
   }
-  __syncthreads();
+  lds_barrier();
 }
 
 // The tokens and pairs of expert e's rows.
@@ -430,7 +439,7 @@ __device__ __forceinline__ void list_rows(const TokArgs &a, Plan &p, const uint1
     const bool hit = q < a.P && ids[q] == (uint16_t)e;
     const uint64_t m = __ballot(hit);
     if (lane == 0) p.wcnt[wave] = __popcll(m);
-    __syncthreads();
+    lds_barrier();
     int base = n;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
@@ -442,7 +451,7 @@ __device__ __forceinline__ void list_rows(const TokArgs &a, Plan &p, const uint1
       p.tok[i] = (int)a.dtopk.div((uint32_t)q);
       p.pair[i] = q;
     }
-    __syncthreads();
+    lds_barrier();
   }
 }
 
@@ -496,6 +505,7 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
   constexpr int kX = 2;   // token vectors a thread has in flight
   constexpr int kOut = (MT * 256 + kNT - 1) / kNT;  // channels x columns per thread
   __shared__ Plan plan;
+  __shared__ float rsl[2 * MT * kTile];  // factors of the item's rows
   uint16_t *ids = reinterpret_cast<uint16_t *>(g_tok_lds);
   char *xrows = g_tok_lds + a.idb;
   // scales and zero points of the item's rows (MT * 16 gate rows, then the up
@@ -562,7 +572,7 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
   const int units = a.rsc.n % 8 == 0 ? 2 * MT * kTile * (a.rsc.n / 8) : 0;
   constexpr int kPf = kSb || kS ? 4 : 1;  // units a thread requests ahead
   uint2 pf[kPf];
-  float rsn[kOut][2];  // factors of the channels that this thread finishes, next item's
+  float rsv = 0.0f;
   // what an item needs besides its codes, requested before them: loads return in order
   auto request = [&](int it) {
     const int tid = anew(threadIdx.x);
@@ -576,18 +586,15 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
           pf[j] = *reinterpret_cast<const uint2 *>(sbase + row * a.rsc.n + o);
       }
     }
-    const int sl = (int)a.dny.div((uint32_t)it), y = it - sl * a.ny;
-    const int e = __builtin_amdgcn_readfirstlane(plan.act[sl]);
-#pragma unroll
-    for (int j = 0; j < kOut; ++j) {
-      const int i = tid + j * kNT, f = (y * MT + (i >> 8)) * kTile + (i & 15);
-      const bool in = i < MT * 256 && f < a.F;
-      rsn[j][0] = in ? row_scale<FMT, MODE>(w, e, (size_t)e * w.N + f) : 0.0f;
-      rsn[j][1] = in ? row_scale<FMT, MODE>(w, e, (size_t)e * w.N + a.F + f) : 0.0f;
+    size_t row;
+    if (tid < 2 * MT * kTile && item_row(it, tid, row)) {
+      const int sl = (int)a.dny.div((uint32_t)it);
+      rsv = row_scale<FMT, MODE>(w, plan.act[sl], row);
     }
   };
   auto store_scales = [&](int it, bool requested) {
     const int tid = anew(threadIdx.x);
+    if (requested && tid < 2 * MT * kTile) rsl[tid] = rsv;
     if (kSb || kS) {
       if (requested) {
 #pragma unroll
@@ -648,27 +655,23 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
     return s;
   };
 
-  point(it0);
-  request(it0);
-  load(raw[0], wk * kU);
+  // A turn computes pass (it, c0), requests what the next one needs, and adds
+  // the shares' sums up while that arrives; the first turn only requests.
   int cur = -1, staged = -1;  // the listed expert, the column group in LDS
-  for (int it = it0; it < it1; ++it) {
+  int it = it0, c0 = -1;
+  while (true) {
+    const bool run = c0 >= 0;
     const int sl = (int)a.dny.div((uint32_t)it), y = it - sl * a.ny;
     const int e = __builtin_amdgcn_readfirstlane(plan.act[sl]);
     const int n = __builtin_amdgcn_readfirstlane(plan.cnt[e]);
     const int off = __builtin_amdgcn_readfirstlane(plan.off[e]);
-    if (sl != cur) {
-      list_rows(a, plan, ids, e);
-      cur = sl;
-      staged = -1;
-    }
-    float rs[kOut][2];
-#pragma unroll
-    for (int j = 0; j < kOut; ++j) {
-      rs[j][0] = rsn[j][0];
-      rs[j][1] = rsn[j][1];
-    }
-    for (int c0 = 0; c0 < n; c0 += a.ncol) {
+    f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    if (run) {
+      if (sl != cur) {
+        list_rows(a, plan, ids, e);
+        cur = sl;
+        staged = -1;
+      }
       store_scales(it, c0 == 0);
       const int nc = min(a.ncol, n - c0), nvec = nc * vpr;
       // ---- the tokens' grid values into LDS, a row's vectors beyond K zero
@@ -694,10 +697,9 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
         }
         staged = c0;
       }
-      __syncthreads();
+      lds_barrier();
 
       // ---- this wave's chunks of the contraction, two batches of loads in turn
-      f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
       const char *xs = xrows + min(col, nc - 1) * xstride + kq * kSeg * 2;
       const int rg = wm * kTile, ru = (MT + wm) * kTile;
       auto compute = [&](Codes (&r)[kU][2], int cb) {
@@ -733,14 +735,19 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
         load(raw[0], cb + 2 * kU * kWK);
         compute(raw[1], cb + kU * kWK);
       }
-      // the next pass's first weights: this item's next columns, or the next item
-      const bool more_c = c0 + a.ncol < n;
-      if (!more_c && it + 1 < it1) {
-        point(it + 1);
-        request(it + 1);
+    }
+    // the next pass: this item's next columns, or the next item
+    const int nit = !run || c0 + a.ncol < n ? it : it + 1;
+    const int nc0 = run && nit == it ? c0 + a.ncol : 0;
+    if (nit < it1) {
+      if (nc0 == 0) {
+        point(nit);
+        request(nit);
       }
-      if (more_c || it + 1 < it1) load(raw[0], wk * kU);
-
+      load(raw[0], wk * kU);
+    }
+    if (run) {
+      const int nc = min(a.ncol, n - c0);
       if (y == 0 && c0 == 0 && tid < n) {  // what the down kernel needs of this expert's rows
         const int q = plan.pair[tid], t = plan.tok[tid];
         float v = a.probs[q];
@@ -750,10 +757,10 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
         a.pw[off + tid] = v;
       }
       // ---- the shares' sums, SwiGLU, FQ_a2. Each wave holds its group's tiles.
-      __syncthreads();
+      lds_barrier();
       red[(wave * 2 + 0) * 64 + lane] = acc[0];
       red[(wave * 2 + 1) * 64 + lane] = acc[1];
-      __syncthreads();
+      lds_barrier();
       // channel f of column c: 16 consecutive lanes hold a group's 16 channels
       const int tid_e = anew(threadIdx.x);
 #pragma unroll
@@ -770,8 +777,8 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
           hg += rf[k * 512 + idx];
           hu += rf[k * 512 + 256 + idx];
         }
-        hg = hg * rs[j][0] * q1.s;
-        hu = hu * rs[j][1] * q1.s;
+        hg = hg * rsl[m * kTile + f] * q1.s;
+        hu = hu * rsl[(MT + m) * kTile + f] * q1.s;
         float av[2] = {hg * sigmoid_hw(hg) * hu, 0.0f};
         float theta = 0.0f;
         if (q2.fmt == FQ_FMT_NVFP4) {
@@ -787,8 +794,11 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
         if (c < nc)
           a.a[(size_t)(off + c0 + c) * a.arow + a_index(a.d.seg, g * kTile + f)] = (uint16_t)v;
       }
-      __syncthreads();
+      lds_barrier();
     }
+    if (nit >= it1) break;
+    it = nit;
+    c0 = nc0;
   }
 }
 
@@ -816,7 +826,7 @@ __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
   const int na = a.nact[0];
   if (tid < min(a.P, a.E)) act[tid] = a.act[tid];  // behind na: stale, not used
   for (int i = tid; i < kWavesD * a.T * 8; i += kNTd) accs[i] = 0.0f;
-  __syncthreads();
+  lds_barrier();
 
   const int nch = w.nch;
   const int col = lane & 15, kq = lane >> 4;
@@ -987,7 +997,7 @@ __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
       if (t.u >= pairs * kp) break;
     }
   }
-  __syncthreads();
+  lds_barrier();
 
   for (int i = tid; i < a.T * 8; i += kNTd) {
     float v = 0.0f;
@@ -1158,6 +1168,7 @@ void launch_moe_tokens(const uint16_t *x, int T, int H, int F, const int32_t *id
   // blocks: two to a CU, at most one per item
   const long items = (long)slots * a.ny;
   const int blocks = (int)(items < 512 ? items : 512);
+  a.dgrid = FastDiv((uint32_t)blocks);
   launch_fmt(w_gu, {false, mt, dim3(blocks), a.idb + a.xb + sums}, a, st);
   launch_fmt(w_d, {true, 0, dim3(H / 8), kWavesD * T * 8 * 4}, a, st);
 }
