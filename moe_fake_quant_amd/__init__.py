@@ -167,8 +167,23 @@ def _p(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it: 0.2 us instead
+# of 2.8 us of every call's 7.3 us on the host.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    return torch.cuda.current_stream().cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
+
+
+def _same_device(t: Optional[torch.Tensor]):
+    """The calls run on the current device's stream; its kernels must not be
+    handed another device's memory."""
+    if t is not None and t.is_cuda and t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
 
 
 @dataclasses.dataclass
@@ -347,6 +362,7 @@ def fq_dequantize_stacked(codes, shape, fmt, group, w_bf16, scale=None, scale_by
 
 def fq_moe_tokens(x, T, H, F, expert_ids, probs, topk, expert_begin, E_local, w_gu: StoredW,
                   w_d: StoredW, aq1: Optional[ActQ], aq2: Optional[ActQ], out, ws=None):
+    _same_device(x)
     _check(_lib.fq_moe_tokens(_p(x), int(T), int(H), int(F), _p(expert_ids), _p(probs), int(topk),
                               int(expert_begin), int(E_local), ctypes.byref(w_gu.c()),
                               ctypes.byref(w_d.c()), _aq(aq1), _aq(aq2), _p(out), _p(ws),
@@ -354,17 +370,20 @@ def fq_moe_tokens(x, T, H, F, expert_ids, probs, topk, expert_begin, E_local, w_
 
 
 def fq_ckpt_save(x, rows, K, n_rows, fmt, group, codes, scale):
+    _same_device(x)
     _check(_lib.fq_ckpt_save(_p(x), int(rows), int(K), _p(n_rows), int(fmt), int(group), _p(codes),
                              _p(scale), _stream()))
 
 
 def fq_ckpt_load(codes, scale, rows, K, n_rows, fmt, group, x):
+    _same_device(codes)
     _check(_lib.fq_ckpt_load(_p(codes), _p(scale), int(rows), int(K), _p(n_rows), int(fmt),
                              int(group), _p(x), _stream()))
 
 
 def fq_swiglu_actfq_ckpt(h, R_max, n_rows, F, aq: Optional[ActQ], fmt, group, a, aq_out, codes,
                          scale):
+    _same_device(h)
     _check(_lib.fq_swiglu_actfq_ckpt(_p(h), int(R_max), _p(n_rows), int(F), _aq(aq), int(fmt),
                                      int(group), _p(a), _p(aq_out), _p(codes), _p(scale),
                                      _stream()))
@@ -372,6 +391,7 @@ def fq_swiglu_actfq_ckpt(h, R_max, n_rows, F, aq: Optional[ActQ], fmt, group, a,
 
 def fq_swiglu_bwd_ckpt(daq, codes, scale, R_max, n_rows, F, fmt, group, aq: Optional[ActQ], dh,
                        aq_out=None, dscale_a=None, ws=None):
+    _same_device(daq)
     _check(_lib.fq_swiglu_bwd_ckpt(_p(daq), _p(codes), _p(scale), int(R_max), _p(n_rows), int(F),
                                    int(fmt), int(group), _aq(aq), _p(dh), _p(aq_out), _p(dscale_a),
                                    _p(ws), _nbytes(ws), _stream()))

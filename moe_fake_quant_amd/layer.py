@@ -23,19 +23,38 @@ second stream of the same priority, each behind the producer of its inputs,
 while the dgrad chain continues on the caller's stream: their persistent
 grids then take over the CUs that a dgrad kernel's last partial round of
 tiles leaves idle. The second stream has a workspace of its own.
+
+With ``ckpt`` the forward keeps h (and the layer input) for the backward as
+8-bit checkpoints instead of bf16: the SwiGLU pass saves h, the backward decodes
+it in registers and re-forms FQ_a(A) for the down projection's dScale. What a
+layer then holds from its forward to its backward is the codes with their
+scales, 2F + H/topk bytes a routed row (and 3 to 25 % for the scales) instead of
+6F + 2H/topk; every other buffer is free in between, and ``scratch_of`` lets the
+layers of a model share one set of them.
+
+After training, ``export()`` gives the stored form of both stacks and
+``forward_tokens`` runs up to 128 tokens on it, as a decoding loop does.
 """
 from __future__ import annotations
 
-from typing import Optional
+from typing import Optional, Tuple
 
 import torch
 
 from . import (ActQ, FMT_FP8_E4M3, FMT_INT4, FMT_INT8, FMT_NONE, FMT_NVFP4, FQ_GROUP_TENSOR,
-               FQ_OP_ACT_SCALE_GRAD, FQ_OP_GEMM_BWD, FQ_OP_GEMM_FWD, FQ_OP_PERMUTE, WeightQ,
-               fq_actfq, fq_grouped_gemm_bwd_scale, fq_grouped_gemm_fwd,
+               FQ_OP_ACT_SCALE_GRAD, FQ_OP_GEMM_BWD, FQ_OP_GEMM_FWD, FQ_OP_MOE_TOKENS,
+               FQ_OP_PERMUTE, StoredW, WeightQ, fq_actfq, fq_ckpt_load, fq_ckpt_save,
+               fq_export_scales, fq_grouped_gemm_bwd_scale, fq_grouped_gemm_fwd,
                fq_grouped_gemm_fwd_tokens, fq_grouped_gemm_wgrad_tokens, fq_moe_combine,
-               fq_moe_combine_bwd, fq_moe_permute, fq_moe_unpermute_reduce, fq_quantize_stacked,
-               fq_swiglu_actfq, fq_swiglu_bwd, fq_workspace_bytes, observer_absmax_init)
+               fq_moe_combine_bwd, fq_moe_permute, fq_moe_tokens, fq_moe_unpermute_reduce,
+               fq_quantize_stacked, fq_swiglu_actfq, fq_swiglu_actfq_ckpt, fq_swiglu_bwd,
+               fq_swiglu_bwd_ckpt, fq_workspace_bytes, observer_absmax_init)
+
+MAX_TOKENS = 128   # of forward_tokens (fq_moe_tokens)
+
+# buffers that hold nothing from a checkpointed layer's forward to its backward
+_SCRATCH = ("xq_tok", "x_back", "a", "aq", "o", "out", "do", "daq", "dh", "dxq", "dx", "ws", "ws2",
+            "side", "ev_do", "ev_dh")
 
 
 def _weight_q(E, N, K, fmt, group, dev) -> WeightQ:
@@ -51,11 +70,16 @@ def _weight_q(E, N, K, fmt, group, dev) -> WeightQ:
 class MoEFakeQuantLayer:
     def __init__(self, w_gu: torch.Tensor, w_d: torch.Tensor, wfmt: int, afmt: int, T_max: int,
                  topk: int, expert_begin: int = 0, group: Optional[int] = None,
-                 learn_act_scales: bool = False):
+                 learn_act_scales: bool = False, ckpt: Optional[Tuple[int, int]] = None,
+                 scratch_of: Optional["MoEFakeQuantLayer"] = None):
         """w_gu [E, 2F, H], w_d [E, H, F] bf16 on the device (frozen). group None =
         one scale per output channel (group = K of each stack); FQ_GROUP_TENSOR =
         one scale per expert matrix (int8 / fp8). learn_act_scales:
-        the backward also produces the activation-scale gradients (FP8 / INT8)."""
+        the backward also produces the activation-scale gradients (FP8 / INT8).
+        ckpt (fmt, group): FMT_INT8 or FMT_FP8_E4M3 checkpoints of h and the
+        input (group as in fq_ckpt_save, dividing F and H). scratch_of: another
+        checkpointed layer of the same sizes and formats, on the same stream,
+        whose buffers this one shares: out and dx hold the last layer's."""
         assert w_gu.dtype == torch.bfloat16 and w_d.dtype == torch.bfloat16
         self.dev = w_gu.device
         self.E, F2, self.H = w_gu.shape
@@ -72,6 +96,20 @@ class MoEFakeQuantLayer:
         g_d = group or self.F
         self.q_gu = _weight_q(*self.shape_gu, wfmt, g_gu, self.dev)
         self.q_d = _weight_q(*self.shape_d, wfmt, g_d, self.dev)
+        if ckpt is not None:
+            fmt, cg = ckpt
+            if fmt not in (FMT_INT8, FMT_FP8_E4M3) or not 16 <= cg <= 512 or cg & (cg - 1) \
+                    or self.F % cg or self.H % cg:
+                raise ValueError("ckpt is (FMT_INT8 or FMT_FP8_E4M3, a power of two from 16 to 512 "
+                                 f"that divides F={self.F} and H={self.H}), not {ckpt}")
+        self.ckpt = ckpt
+        if scratch_of is not None:
+            o = scratch_of
+            if ckpt is None or o.ckpt is None:
+                raise ValueError("only checkpointed layers can share their buffers")
+            if (o.dev, o.E, o.H, o.F, o.T_max, o.topk) != (self.dev, self.E, self.H, self.F, T_max,
+                                                           topk):
+                raise ValueError("layers that share buffers must have the same sizes and device")
         f32 = dict(dtype=torch.float32, device=self.dev)
         bf = dict(dtype=torch.bfloat16, device=self.dev)
         i32 = dict(dtype=torch.int32, device=self.dev)
@@ -84,20 +122,35 @@ class MoEFakeQuantLayer:
         self.row_of = torch.empty(T_max, topk, **i32)
         self.seg = torch.empty(self.E + 1, **i32)
         self.n_rows = self.seg[self.E:]
+        if ckpt is not None:
+            cg = ckpt[1]
+            u8 = dict(dtype=torch.uint8, device=self.dev)
+            self.h_codes = torch.empty(R, 2 * F, **u8)
+            self.h_scale = torch.empty(R, 2 * F // cg, **f32)
+            self.x_codes = torch.empty(T_max, H, **u8)
+            self.x_scale = torch.empty(T_max, H // cg, **f32)
         # the expert input as token rows: FQ_a(x) once per token; the gate_up
         # GEMMs read routed row r as token row perm[r] / topk
-        self.xq_tok = torch.empty(T_max, H, **bf)
         self._x_tok = None
-        self.h = torch.empty(R, 2 * F, **bf)
-        self.a = torch.empty(R, F, **bf)
-        self.aq = torch.empty(R, F, **bf)
-        self.o = torch.empty(R, H, **bf)
-        self.out = torch.empty(T_max, H, **bf)
-        self.do = torch.empty(R, H, **bf)
-        self.daq = torch.empty(R, F, **bf)
-        self.dh = torch.empty(R, 2 * F, **bf)
-        self.dxq = torch.empty(R, H, **bf)
-        self.dx = torch.empty(T_max, H, **bf)
+        if scratch_of is not None:
+            for name in _SCRATCH:
+                setattr(self, name, getattr(scratch_of, name))
+            self.h = self.dh
+        else:
+            self.xq_tok = torch.empty(T_max, H, **bf)
+            self.a = torch.empty(R, F, **bf)
+            self.aq = torch.empty(R, F, **bf)
+            self.o = torch.empty(R, H, **bf)
+            self.out = torch.empty(T_max, H, **bf)
+            self.do = torch.empty(R, H, **bf)
+            self.daq = torch.empty(R, F, **bf)
+            self.dh = torch.empty(R, 2 * F, **bf)
+            # a checkpointed h is read once, by the pass that saves it, and dh
+            # is first written after that
+            self.h = torch.empty(R, 2 * F, **bf) if ckpt is None else self.dh
+            self.x_back = None if ckpt is None else torch.empty(T_max, H, **bf)
+            self.dxq = torch.empty(R, H, **bf)
+            self.dx = torch.empty(T_max, H, **bf)
         self.ds_gu = torch.empty_like(self.q_gu.scale)
         self.ds_d = torch.empty_like(self.q_d.scale)
         self.dzp_gu = torch.empty_like(self.q_gu.scale) if wfmt == FMT_INT4 else None
@@ -107,18 +160,19 @@ class MoEFakeQuantLayer:
         self.learn_act_scales = learn_act_scales
         self.ds_a1 = torch.zeros(1, **f32) if learn_act_scales else None
         self.ds_a2 = torch.zeros(1, **f32) if learn_act_scales else None
-        ws = max(fq_workspace_bytes(FQ_OP_PERMUTE, (self.E, 0, 0), self.R_max, 0),
-                 fq_workspace_bytes(FQ_OP_ACT_SCALE_GRAD, (1, T_max, H), 0, 0),
-                 fq_workspace_bytes(FQ_OP_ACT_SCALE_GRAD, (1, R, F), 0, 0),
-                 fq_workspace_bytes(FQ_OP_GEMM_FWD, self.shape_gu, R, 0),
-                 fq_workspace_bytes(FQ_OP_GEMM_FWD, self.shape_d, R, 0),
-                 fq_workspace_bytes(FQ_OP_GEMM_BWD, self.shape_gu, R, 0),
-                 fq_workspace_bytes(FQ_OP_GEMM_BWD, self.shape_d, R, 0), 256)
-        self.ws = torch.empty(ws, dtype=torch.uint8, device=self.dev)
-        self.ws2 = torch.empty(ws, dtype=torch.uint8, device=self.dev)
-        self.side = torch.cuda.Stream(device=self.dev)   # default priority
-        self.ev_do = torch.cuda.Event()
-        self.ev_dh = torch.cuda.Event()
+        if scratch_of is None:
+            ws = max(fq_workspace_bytes(FQ_OP_PERMUTE, (self.E, 0, 0), self.R_max, 0),
+                     fq_workspace_bytes(FQ_OP_ACT_SCALE_GRAD, (1, T_max, H), 0, 0),
+                     fq_workspace_bytes(FQ_OP_ACT_SCALE_GRAD, (1, R, F), 0, 0),
+                     fq_workspace_bytes(FQ_OP_GEMM_FWD, self.shape_gu, R, 0),
+                     fq_workspace_bytes(FQ_OP_GEMM_FWD, self.shape_d, R, 0),
+                     fq_workspace_bytes(FQ_OP_GEMM_BWD, self.shape_gu, R, 0),
+                     fq_workspace_bytes(FQ_OP_GEMM_BWD, self.shape_d, R, 0), 256)
+            self.ws = torch.empty(ws, dtype=torch.uint8, device=self.dev)
+            self.ws2 = torch.empty(ws, dtype=torch.uint8, device=self.dev)
+            self.side = torch.cuda.Stream(device=self.dev)   # default priority
+            self.ev_do = torch.cuda.Event()
+            self.ev_dh = torch.cuda.Event()
         self.overlap_wgrad = True
         self.T = 0
 
@@ -171,8 +225,13 @@ class MoEFakeQuantLayer:
         T = x.shape[0]
         self.route(expert_ids)
         self._gate_up_fwd(x, T)
-        fq_swiglu_actfq(self.h, self.R_max, self.n_rows, self.F, self.aq2,
-                        self.a if keep_a else None, self.aq)
+        if self.ckpt is None:
+            fq_swiglu_actfq(self.h, self.R_max, self.n_rows, self.F, self.aq2,
+                            self.a if keep_a else None, self.aq)
+        else:
+            fq_ckpt_save(x, T, self.H, None, *self.ckpt, self.x_codes[:T], self.x_scale[:T])
+            fq_swiglu_actfq_ckpt(self.h, self.R_max, self.n_rows, self.F, self.aq2, *self.ckpt,
+                                 self.a if keep_a else None, self.aq, self.h_codes, self.h_scale)
         fq_grouped_gemm_fwd(self.aq, self.R_max, self.seg, self.shape_d, None, self.wfq_d,
                             self.q_d, None, self.o, self.ws)
         fq_moe_combine(self.o, probs, self.row_of[:T], T, self.topk, self.H, self.out[:T])
@@ -212,8 +271,24 @@ class MoEFakeQuantLayer:
         with torch.cuda.stream(self.side):
             launch(self.ws2)
 
-    def backward(self, x: torch.Tensor, probs: torch.Tensor, dout: torch.Tensor):
-        T = x.shape[0]
+    def _restore_input(self, x: Optional[torch.Tensor], T: int) -> torch.Tensor:
+        """The layer input in the backward of a checkpointed layer (x, or the
+        saved one for None), and again the gate_up operand made from it."""
+        if x is None:
+            x = self.x_back[:T]
+            fq_ckpt_load(self.x_codes[:T], self.x_scale[:T], T, self.H, None, *self.ckpt, x)
+        if self.afmt == FMT_NONE:
+            self._x_tok = x
+        else:
+            fq_actfq(x, T, self.H, self.aq1, self.xq_tok)
+            self._x_tok = self.xq_tok
+        return x
+
+    def backward(self, x: Optional[torch.Tensor], probs: torch.Tensor, dout: torch.Tensor):
+        """x None (checkpointed layers): the input is taken from its checkpoint."""
+        T = self.T if x is None else x.shape[0]
+        if x is None and self.ckpt is None:
+            raise ValueError("backward without x needs a checkpointed layer")
         main = torch.cuda.current_stream(self.dev)
         if self.overlap_wgrad:
             # the side stream's previous step (and anything else the caller
@@ -225,12 +300,21 @@ class MoEFakeQuantLayer:
         # the dgrad is enqueued first: it leads the chain to dX
         fq_grouped_gemm_bwd_scale(self.do, None, self.R_max, self.seg, self.shape_d, self.w_d,
                                   self.wfq_d, self.q_d, None, self.daq, None, None, self.ws)
-        self._wgrad(self.ev_do, lambda ws: fq_grouped_gemm_bwd_scale(
+        down_wgrad = lambda ws: fq_grouped_gemm_bwd_scale(  # noqa: E731
             self.do, self.aq, self.R_max, self.seg, self.shape_d, self.w_d, self.wfq_d, self.q_d,
-            None, None, self.ds_d, self.dzp_d, ws))
-        fq_swiglu_bwd(self.daq, self.h, self.R_max, self.n_rows, self.F, self.aq2, self.dh,
-                      self.ds_a2, self.ws)
-        self.ev_dh.record(main)
+            None, None, self.ds_d, self.dzp_d, ws)
+        if self.ckpt is None:
+            self._wgrad(self.ev_do, down_wgrad)
+            fq_swiglu_bwd(self.daq, self.h, self.R_max, self.n_rows, self.F, self.aq2, self.dh,
+                          self.ds_a2, self.ws)
+            self.ev_dh.record(main)
+        else:
+            # FQ_a(A) comes out of the SwiGLU backward, so this wgrad starts behind it
+            fq_swiglu_bwd_ckpt(self.daq, self.h_codes, self.h_scale, self.R_max, self.n_rows,
+                               self.F, *self.ckpt, self.aq2, self.dh, self.aq, self.ds_a2, self.ws)
+            x = self._restore_input(x, T)
+            self.ev_dh.record(main)
+            self._wgrad(self.ev_dh, down_wgrad)
         fq_grouped_gemm_bwd_scale(self.dh, None, self.R_max, self.seg, self.shape_gu, self.w_gu,
                                   self.wfq_gu, self.q_gu, None, self.dxq, None, None, self.ws)
         x_tok = self._x_tok
@@ -250,3 +334,57 @@ class MoEFakeQuantLayer:
         self.quantize_weights()
         self.forward(x, expert_ids, probs)
         return self.backward(x, probs, dout)
+
+    # ----------------------------------------------------------- serving --
+    def _stored(self, w, shape, q, st: Optional[StoredW]) -> StoredW:
+        E, N, K = shape
+        if st is None:
+            four = q.fmt in (FMT_INT4, FMT_NVFP4)
+            u8 = dict(dtype=torch.uint8, device=self.dev)
+            st = StoredW(q.fmt, q.group, torch.empty(E * N * K // (2 if four else 1), **u8))
+            if q.fmt == FMT_NVFP4:
+                st.scale_bytes = torch.empty(E * N * K // 16, **u8)
+                st.global_scale = torch.empty_like(q.global_scale)
+            else:
+                st.scale = torch.empty_like(q.scale)
+                if q.fmt == FMT_INT4:
+                    st.zero_point_bytes = torch.empty(E * N * K // q.group, **u8)
+        fq_quantize_stacked(w, shape, q, None, st.codes)
+        if q.fmt == FMT_NVFP4:
+            st.global_scale.copy_(q.global_scale)
+            fq_export_scales(shape, q, st.scale_bytes, None)
+        else:
+            st.scale.copy_(q.scale)
+            if q.fmt == FMT_INT4:
+                fq_export_scales(shape, q, None, st.zero_point_bytes)
+        return st
+
+    def export(self) -> Tuple[StoredW, StoredW]:
+        """Both stacks in their stored form (codes and scales of the present
+        quantizer parameters), which forward_tokens reads from now on. A later
+        export overwrites them in place, so a captured decoding step stays valid."""
+        old = getattr(self, "stored", None) or (None, None)
+        self.stored = (self._stored(self.w_gu, self.shape_gu, self.q_gu, old[0]),
+                       self._stored(self.w_d, self.shape_d, self.q_d, old[1]))
+        if old[0] is None:
+            n = fq_workspace_bytes(FQ_OP_MOE_TOKENS, (self.E, self.H, self.F),
+                                   MAX_TOKENS * self.topk, self.topk)
+            self.tok_ws = torch.empty(n, dtype=torch.uint8, device=self.dev)
+            self.tok_out = torch.empty(MAX_TOKENS, self.H, dtype=torch.bfloat16, device=self.dev)
+        return self.stored
+
+    def forward_tokens(self, x: torch.Tensor, expert_ids: torch.Tensor,
+                       probs: torch.Tensor) -> torch.Tensor:
+        """The layer for up to 128 tokens over the exported stacks: two kernels,
+        only the experts that the tokens name are read. The result is the
+        layer's own buffer, overwritten by the next call; calls of one layer
+        share a workspace and must not overlap."""
+        if getattr(self, "stored", None) is None:
+            raise ValueError("forward_tokens needs export() first")
+        T = x.shape[0]
+        if expert_ids.shape != (T, self.topk) or probs.shape != (T, self.topk):
+            raise ValueError(f"expert_ids and probs must be [{T}, {self.topk}]")
+        out = self.tok_out[:T]
+        fq_moe_tokens(x, T, self.H, self.F, expert_ids, probs, self.topk, self.expert_begin,
+                      self.E, *self.stored, self.aq1, self.aq2, out, self.tok_ws)
+        return out

@@ -54,8 +54,8 @@ class Call:
         F.fq_moe_tokens(self.x, c["T"], c["H"], c["F"], self.ids, self.p, c["topk"], c["begin"],
                         c["E"], self.gu, self.d, self.a1, self.a2, self.out[:c["T"]], self.ws)
 
-    def check(self):
-        ref, tol = reference(self.c)
+    def check(self, against=None):
+        ref, tol = against or reference(self.c)
         torch.cuda.synchronize()
         got = bf16_vals(host_bits(self.out))
         T = self.c["T"]
@@ -234,31 +234,31 @@ def test_two_streams_with_workspaces_of_their_own():
 
 
 def test_default_workload_layer():
-    """H 2048, F 768, 128 experts, top 8 (a few tokens, random codes): every
-    expert's codes at its own offset, the splits of the down projection."""
+    """H 2048, F 768, top 8: eight experts alone, and the same eight scattered
+    among 128 (every expert's codes at its own offset)."""
     rng = np.random.default_rng(80)
-    for T in (1, 19):
+    for T in (1, 9):
         c = make(seed=81, T=T, E=8, H=2048, F=768, topk=8, fmt=O.FMT_NVFP4, group=16,
                  afmt=O.FMT_NVFP4)
+        ref = reference(c)
         small = Call(c)
         small.run()
-        small.check()
-        # the same eight experts scattered among 128: the same bits
+        small.check(ref)
         place = np.sort(rng.choice(128, 8, replace=False))
-        big = dict(c, E=128, ids=place[c["ids"]].astype(np.int32))
-        for k in ("gu", "d"):
-            fmt, group, bits, (s, zp, g) = c[k]
-            up = lambda t, fill: np.concatenate(  # noqa: E731
-                [np.full((128 - 8,) + t.shape[1:], fill, t.dtype), t])
-            order = np.concatenate([np.setdiff1d(np.arange(128), place), place])
-            inv = np.argsort(order)
-            big[k] = (fmt, group, up(bits, 0x3F80)[inv], (up(s, 1)[inv], None, up(g, 1)[inv]))
-        b = Call(big)
-        b.run()
-        torch.cuda.synchronize()
-        ref, tol = reference(c)
-        got = bf16_vals(host_bits(b.out))[:T]
-        assert np.all(np.abs(got - ref) <= tol + 2.0 ** -8 * (np.abs(ref) + tol))
+        at = torch.from_numpy(place).cuda()
+        big = Call(c)
+        for st, per in ((big.gu, 2 * 768 * 2048), (big.d, 2048 * 768)):
+            for name, n in (("codes", per // 2), ("scale_bytes", per // 16), ("global_scale", 1)):
+                src = getattr(st, name).reshape(8, n)
+                dst = torch.full((128, n), 0x22, dtype=torch.uint8, device="cuda").to(src.dtype)
+                dst[at] = src
+                setattr(st, name, dst.reshape(-1))
+        big.ids = dev_i32(place[c["ids"]])
+        F.fq_moe_tokens(big.x, T, 2048, 768, big.ids, big.p, 8, 0, 128, big.gu, big.d, big.a1,
+                        big.a2, big.out[:T], torch.empty(
+                            F.fq_workspace_bytes(F.FQ_OP_MOE_TOKENS, (128, 2048, 768), T * 8, 8),
+                            dtype=torch.uint8, device="cuda"))
+        big.check(ref)
 
 
 def test_refusals_with_device_tensors():
