@@ -478,10 +478,9 @@ fq_status fq_moe_unpermute_reduce(const uint16_t *dxq_bf16, const int32_t *row_o
  *   E_local); a token without such a slot gets 0. A token may name an expert
  *   twice (the weights add). Ids outside the range are not local.
  *   W = value(code) * scale as fq_dequantize_stacked defines it, without its
- *   rounding to bf16, except where the weight group is smaller than 64 (int8,
- *   fp8) or not a multiple of 128 (int4) and not the whole row: then W is
- *   the bf16 fake-quant value. Sums are fp32, in a fixed order (bitwise
- *   reproducible).
+ *   rounding to bf16, except where the weight group is not a multiple of 64
+ *   (int8, fp8), resp. 128 (int4), and not the whole row: then W is the bf16
+ *   fake-quant value. Sums are fp32, in a fixed order (bitwise reproducible).
  * fq_stored_w: fmt FQ_FMT_*, group as in fq_weight_q (int4: the whole row or a
  *   multiple of 32), codes [E, N, K] packed as exported (NONE: the raw bf16
  *   stack, group and the scales unused); scale (int8, fp8, int4),
@@ -490,7 +489,9 @@ fq_status fq_moe_unpermute_reduce(const uint16_t *dxq_bf16, const int32_t *row_o
  * x_bf16, out_bf16 [T, H]; expert_ids, probs [T, topk]. out must not overlap x.
  * codes and the scale pointers 16-byte aligned (global_scale: 4-byte).
  * 0 <= T <= 128 (for more tokens the grouped GEMM calls are the path),
- * 1 <= topk <= 64, E_local <= 1024, H and F % 16 == 0 and <= 16384.
+ * 1 <= topk <= 64, E_local <= 1024, H and F % 16 == 0 and <= 16384. Very wide
+ * rows of small int8 / fp8 / int4 groups whose scales do not fit into LDS (16
+ * rows times H/group fp32 scales, near H = 16384) are FQ_ERR_UNSUPPORTED.
  * Workspace: fq_workspace_bytes(FQ_OP_MOE_TOKENS, {E_local, H, F}, T * topk,
  * topk). Calls that may overlap on the device need workspaces of their own
  * (two graphs captured over one workspace must not be replayed at once).

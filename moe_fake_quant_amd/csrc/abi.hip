@@ -835,6 +835,11 @@ fq_status fq_moe_tokens(const uint16_t *x, int32_t T, int32_t H, int32_t F, cons
   FQ_CHECK_ARG((!x || aligned16(x)) && (!out || aligned16(out)),
                "bf16 tensors must be 16-byte aligned");
   if (T == 0) return FQ_OK;
+  // a row's scales of small groups pass through LDS beside a staged token row
+  const size_t lds = moe_tokens_lds_bytes(T, H, F, topk, E, *w_gu, *w_d);
+  FQ_CHECK_SUPPORTED(lds <= (160u << 10),
+                     "w_gu: rows of H=%d in groups of %d need %zu bytes of LDS, 160 KB exist", H,
+                     w_gu->group, lds);
   const size_t need = moe_tokens_ws_bytes(T, topk, E, F);
   if (!ws || ws_bytes < need) {
     set_error("fq_moe_tokens: workspace %zu bytes < %zu needed", ws_bytes, need);

@@ -67,6 +67,8 @@ void launch_swiglu_bwd_ckpt(const uint16_t *daq, const uint8_t *codes, const flo
 // One MoE layer for T <= kTokMax tokens over stored weights (workspace bytes below).
 constexpr int kTokMax = 128;
 size_t moe_tokens_ws_bytes(int T, int topk, int E, int F);
+size_t moe_tokens_lds_bytes(int T, int H, int F, int topk, int E, const fq_stored_w &w_gu,
+                            const fq_stored_w &w_d);
 void launch_moe_tokens(const uint16_t *x, int T, int H, int F, const int32_t *ids,
                        const float *probs, int topk, int ebegin, int E, const fq_stored_w &w_gu,
                        const fq_stored_w &w_d, int afmt1, const float *as1, int afmt2,

@@ -1032,6 +1032,8 @@ TokStack tok_stack(const fq_stored_w &w, int N, int K, int afmt) {
   return t;
 }
 
+constexpr int kMtTail = 2;  // channel groups per gate_up item where rows end inside a chunk
+
 struct Launch {
   bool down;
   int mt;  // channel groups per gate_up block
@@ -1039,25 +1041,26 @@ struct Launch {
   int lds;
 };
 
+template <int FMT, int MODE, bool F16, bool WHOLE>
+void launch_down(const Launch &l, const TokArgs &a, hipStream_t st) {
+  hipLaunchKernelGGL((k_tok_down<FMT, MODE, F16, WHOLE>), l.grid, dim3(kNTd), l.lds, st, a);
+}
+template <int FMT, int MODE, bool F16, bool WHOLE, int MT>
+void launch_gate_up(const Launch &l, const TokArgs &a, hipStream_t st) {
+  hipLaunchKernelGGL((k_tok_gate_up<FMT, MODE, F16, WHOLE, MT>), l.grid, dim3(kNT), l.lds, st, a);
+}
+
 template <int FMT, int MODE, bool F16>
 void launch_one(const Launch &l, const TokArgs &a, hipStream_t st) {
-#define FQ_GU(WHOLE, MT)                                                                        \
-  hipLaunchKernelGGL((k_tok_gate_up<FMT, MODE, F16, WHOLE, MT>), l.grid, dim3(kNT), l.lds, st, a)
-  if (l.down) {
-    if (a.d.whole)
-      hipLaunchKernelGGL((k_tok_down<FMT, MODE, F16, true>), l.grid, dim3(kNTd), l.lds, st, a);
-    else
-      hipLaunchKernelGGL((k_tok_down<FMT, MODE, F16, false>), l.grid, dim3(kNTd), l.lds, st, a);
-  } else if (!a.gu.whole) {  // (two channel groups: see launch_moe_tokens)
-    FQ_GU(false, 2);
-  } else if (l.mt == 4) {
-    FQ_GU(true, 4);
-  } else if (l.mt == 2) {
-    FQ_GU(true, 2);
-  } else {
-    FQ_GU(true, 1);
+  // groups of whole chunks make rows of whole chunks
+  if constexpr (MODE != kPost) {
+    if (l.down && !a.d.whole) return launch_down<FMT, MODE, F16, false>(l, a, st);
+    if (!l.down && !a.gu.whole) return launch_gate_up<FMT, MODE, F16, false, kMtTail>(l, a, st);
   }
-#undef FQ_GU
+  if (l.down) launch_down<FMT, MODE, F16, true>(l, a, st);
+  else if (l.mt == 4) launch_gate_up<FMT, MODE, F16, true, 4>(l, a, st);
+  else if (l.mt == 2) launch_gate_up<FMT, MODE, F16, true, 2>(l, a, st);
+  else launch_gate_up<FMT, MODE, F16, true, 1>(l, a, st);
 }
 
 template <int FMT>
@@ -1100,10 +1103,71 @@ TokWs tok_ws(int T, int topk, int E, int F) {
   return w;
 }
 
+
+// The gate_up launch: items, token rows staged at a time, LDS.
+Launch gate_up_launch(TokArgs &a, const fq_stored_w &w_gu) {
+  // A's zero tail up to whole chunks of the down projection counts as channels
+  a.arow = a.d.nch * a.d.seg * 4;
+  a.agroups = a.arow / kTile;
+  // channel groups per item: the most that leave two items to a block (fewer
+  // items spread the staging of the tokens over more weights, more of them keep
+  // every CU busy: one token of the default layer takes 13 us with 1 group, the
+  // 64-token batch 63 with 4)
+  const int slots = a.P < a.E ? a.P : a.E;
+  int mt = 4;
+  while (mt > 1 && (long)slots * ((a.agroups + mt - 1) / mt) < 1024) mt /= 2;
+  // bytes of a row's scales, fewer channels to an item where they are many
+  const int f = w_gu.fmt, ng = a.gu.groups;
+  const bool grouped = f != FQ_FMT_NONE && f != FQ_FMT_NVFP4 && ng > 1;
+  a.rsc = row_bytes(f == FQ_FMT_NVFP4 ? a.gu.K / 16 : grouped ? 4 * ng : 0);
+  a.rzp = row_bytes(f == FQ_FMT_INT4 ? ng : 0);
+  const int per_row = (a.rsc.n ? a.rsc.stride : 0) + (a.rzp.n ? a.rzp.stride : 0);
+  while (mt > 1 && 2 * mt * kTile * per_row > (20 << 10)) mt /= 2;
+  if (!a.gu.whole) mt = kMtTail;
+  a.ny = (a.agroups + mt - 1) / mt;
+  a.dny = FastDiv((uint32_t)a.ny);
+  // token rows staged at a time: 16 columns of an MFMA, or what leaves two
+  // blocks to a CU (80 KB, 14 of them the plan), at least one
+  const int chunk = a.gu.seg * 4, row = xrow_bytes(a.gu.K, chunk);
+  int sums = 2 * mt * kTile * per_row;
+  if (sums < kRedBytes) sums = kRedBytes;
+  a.idb = (a.P * 2 + 15) / 16 * 16;
+  int nc = ((80 << 10) - (14 << 10) - a.idb - sums) / row;
+  nc = nc < 1 ? 1 : nc > 16 ? 16 : nc;
+  a.ncol = nc < a.T ? nc : a.T;
+  a.xb = a.ncol * row;
+  a.dvpr = FastDiv((uint32_t)(a.gu.nch * (chunk / 8)));
+  a.dncol = FastDiv((uint32_t)a.ncol);
+  // blocks: two to a CU, at most one per item
+  const long items = (long)slots * a.ny;
+  const int blocks = (int)(items < 512 ? items : 512);
+  a.dgrid = FastDiv((uint32_t)blocks);
+  return {false, mt, dim3(blocks), a.idb + a.xb + sums};
+}
+
+void set_sizes(TokArgs &a, int T, int H, int F, int topk, int E, const fq_stored_w &w_gu,
+               const fq_stored_w &w_d, int afmt1, int afmt2) {
+  a.T = T;
+  a.topk = topk;
+  a.P = T * topk;
+  a.E = E;
+  a.H = H;
+  a.F = F;
+  a.gu = tok_stack(w_gu, 2 * F, H, afmt1);
+  a.d = tok_stack(w_d, H, F, afmt2);
+}
+
 }  // namespace
 
 size_t moe_tokens_ws_bytes(int T, int topk, int E, int F) {
   return tok_ws(T, topk, E, F).total;
+}
+
+size_t moe_tokens_lds_bytes(int T, int H, int F, int topk, int E, const fq_stored_w &w_gu,
+                            const fq_stored_w &w_d) {
+  TokArgs a{};
+  set_sizes(a, T, H, F, topk, E, w_gu, w_d, FQ_FMT_NONE, FQ_FMT_NONE);
+  return (size_t)gate_up_launch(a, w_gu).lds + sizeof(Plan) + 2 * 4 * kTile * sizeof(float);
 }
 
 void launch_moe_tokens(const uint16_t *x, int T, int H, int F, const int32_t *ids,
@@ -1112,64 +1176,24 @@ void launch_moe_tokens(const uint16_t *x, int T, int H, int F, const int32_t *id
                        const float *as2, uint16_t *out, void *ws, hipStream_t st) {
   const TokWs o = tok_ws(T, topk, E, F);
   char *b = static_cast<char *>(ws);
-  TokArgs a;
+  TokArgs a{};
+  set_sizes(a, T, H, F, topk, E, w_gu, w_d, afmt1, afmt2);
   a.x = x;
   a.ids = ids;
   a.probs = probs;
-  a.T = T;
-  a.topk = topk;
-  a.P = T * topk;
   a.ebegin = ebegin;
-  a.E = E;
   a.dtopk = FastDiv((uint32_t)topk);
   a.afmt1 = afmt1;
   a.afmt2 = afmt2;
   a.as1 = as1;
   a.as2 = as2;
-  a.gu = tok_stack(w_gu, 2 * F, H, afmt1);
-  a.d = tok_stack(w_d, H, F, afmt2);
-  a.H = H;
-  a.F = F;
   a.a = reinterpret_cast<uint16_t *>(b + o.a);
   a.act = reinterpret_cast<int4 *>(b + o.act);
   a.nact = reinterpret_cast<int32_t *>(b + o.nact);
   a.tok = reinterpret_cast<int32_t *>(b + o.tok);
   a.pw = reinterpret_cast<float *>(b + o.pw);
   a.out = out;
-  // channel groups per gate_up item: the most that leave two items to a block.
-  // A's zero tail up to whole chunks of the down projection counts as channels.
-  a.arow = a.d.nch * a.d.seg * 4;
-  a.agroups = a.arow / kTile;
-  const int slots = a.P < E ? a.P : E;
-  int mt = 4;
-  while (mt > 1 && (long)slots * ((a.agroups + mt - 1) / mt) < 1024) mt /= 2;
-  // bytes of a row's scales, fewer channels to an item where they are many
-  const int f = w_gu.fmt, ng = a.gu.groups;
-  const bool grouped = f != FQ_FMT_NONE && f != FQ_FMT_NVFP4 && ng > 1;
-  a.rsc = row_bytes(f == FQ_FMT_NVFP4 ? H / 16 : grouped ? 4 * ng : 0);
-  a.rzp = row_bytes(f == FQ_FMT_INT4 ? ng : 0);
-  const int per_row = (a.rsc.n ? a.rsc.stride : 0) + (a.rzp.n ? a.rzp.stride : 0);
-  while (mt > 1 && 2 * mt * kTile * per_row > (20 << 10)) mt /= 2;
-  if (!a.gu.whole) mt = 2;
-  a.ny = (a.agroups + mt - 1) / mt;
-  a.dny = FastDiv((uint32_t)a.ny);
-  // token rows staged at a time: 16 columns of an MFMA, or what leaves two
-  // blocks to a CU (80 KB, 14 of them the plan), at least one
-  const int chunk = chunk_of(w_gu.fmt), row = xrow_bytes(H, chunk);
-  int sums = 2 * mt * kTile * per_row;
-  if (sums < kRedBytes) sums = kRedBytes;
-  a.idb = (a.P * 2 + 15) / 16 * 16;
-  int nc = ((80 << 10) - (14 << 10) - a.idb - sums) / row;
-  nc = nc < 1 ? 1 : nc > 16 ? 16 : nc;
-  a.ncol = nc < T ? nc : T;
-  a.xb = a.ncol * row;
-  a.dvpr = FastDiv((uint32_t)(a.gu.nch * (chunk / 8)));
-  a.dncol = FastDiv((uint32_t)a.ncol);
-  // blocks: two to a CU, at most one per item
-  const long items = (long)slots * a.ny;
-  const int blocks = (int)(items < 512 ? items : 512);
-  a.dgrid = FastDiv((uint32_t)blocks);
-  launch_fmt(w_gu, {false, mt, dim3(blocks), a.idb + a.xb + sums}, a, st);
+  launch_fmt(w_gu, gate_up_launch(a, w_gu), a, st);
   launch_fmt(w_d, {true, 0, dim3(H / 8), kWavesD * T * 8 * 4}, a, st);
 }
 

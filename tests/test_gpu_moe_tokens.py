@@ -125,6 +125,14 @@ def test_wide_rows_stage_few_columns():
     run_case(seed=52, T=3, E=1, H=16384, F=16, topk=1, fmt=O.FMT_NVFP4, group=16, afmt=O.FMT_NONE)
 
 
+def test_wide_rows_of_small_groups_and_many_pairs():
+    """The largest use of LDS: an expert row's scales and zero points, and the
+    pairs of 128 tokens that name 64 experts each."""
+    run_case(seed=55, T=2, E=1, H=16384, F=32, topk=1, fmt=O.FMT_INT4, group=32, afmt=O.FMT_NONE)
+    run_case(seed=56, T=128, E=70, H=64, F=32, topk=64, fmt=O.FMT_INT8, group=None,
+             afmt=O.FMT_INT8)
+
+
 def test_wide_f():
     run_case(seed=53, T=3, E=2, H=32, F=4096, topk=2, fmt=O.FMT_INT4, group=None, group_d=128,
              afmt=O.FMT_NONE)

@@ -93,6 +93,10 @@ def test_refusals(pkg):  # noqa: F811
     for bad in (dict(T=129), dict(topk=65), dict(E=1025), dict(H=264), dict(F=136), dict(H=16400),
                 dict(F=16400), dict(gu=w(pkg.FMT_INT4, 16)), dict(d=w(pkg.FMT_INT4, 16))):
         assert call(**bad) == pkg.FQ_ERR_UNSUPPORTED, bad
+    # scales that do not fit into LDS, whatever the rest
+    for H, gu in ((16384, w(pkg.FMT_INT8, 16)), (16368, w(pkg.FMT_FP8_E4M3, 16))):
+        assert call(H=H, F=64, gu=gu, d=w()) == pkg.FQ_ERR_UNSUPPORTED
+        assert b"LDS" in lib.fq_last_error()
     assert lib.fq_moe_tokens(P, 4, 256, 128, P, P, 2, 0, 8, None, ref(w()), None, None, P, P,
                              1 << 40, None) == arg
     need = pkg.fq_workspace_bytes(pkg.FQ_OP_MOE_TOKENS, (8, 256, 128), 8, 2)
