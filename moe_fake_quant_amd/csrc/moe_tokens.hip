@@ -410,13 +410,18 @@ __device__ __forceinline__ int make_plan(const TokArgs &a, Plan &p, uint16_t *id
   return (int)(run >> 16);
 }
 
-// This block's items into p.it: those that begin in its share of the passes (an
+// This block's items: those that begin in its share of the passes (an
 // expert's items count its passes each, so that a hot expert's weigh as much as
 // they take).
-__device__ __forceinline__ void my_items(const TokArgs &a, Plan &p, int na) {
+__device__ __forceinline__ void my_items(const TokArgs &a, Plan &p, int na, int &it0, int &it1) {
   const uint32_t total = (uint32_t)p.pass[na] * a.ny;
   const uint32_t share = a.dgrid.div(total), rest = total - share * gridDim.x;
   const int tid = threadIdx.x;
+  if (p.pass[na] == na) {  // every expert takes one pass: an item is a pass
+    it0 = (int)(blockIdx.x * share + min(blockIdx.x, rest));
+    it1 = (int)((blockIdx.x + 1) * share + min(blockIdx.x + 1, rest));
+    return;
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t b = blockIdx.x + h, at = b * share + min(b, rest);
@@ -428,6 +433,8 @@ __device__ __forceinline__ void my_items(const TokArgs &a, Plan &p, int na) {
     if (tid == 0 && at == total) p.it[h] = na * a.ny;
   }
   lds_barrier();
+  it0 = __builtin_amdgcn_readfirstlane(p.it[0]);
+  it1 = __builtin_amdgcn_readfirstlane(p.it[1]);
 }
 
 // The tokens and pairs of expert e's rows.
@@ -527,9 +534,8 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
     }
   }
   if (na == 0) return;
-  my_items(a, plan, na);
-  const int it0 = __builtin_amdgcn_readfirstlane(plan.it[0]);
-  const int it1 = __builtin_amdgcn_readfirstlane(plan.it[1]);
+  int it0, it1;
+  my_items(a, plan, na, it0, it1);
   if (it0 >= it1) return;
 
   const float rg1 = 1.0f / (6.0f * q1.s), rg2 = 1.0f / (6.0f * q2.s);
