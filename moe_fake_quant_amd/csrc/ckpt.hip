@@ -19,7 +19,11 @@
 // lives from the forward to the backward in bf16: 6F bytes per row become
 // 2F + 8F/group.
 //
-// All passes are HBM-bound streams of 16-byte vectors per lane. The group's
+// All passes are HBM-bound streams of 16-byte vectors per lane, one per thread as
+// in the elementwise passes. Measured: the SwiGLU forward with save 160 us and
+// the backward 182 us at 131072 rows of F = 768 (0.81 and 1.01 GB: 5.1 and 5.6
+// TB/s; a 1 GiB device copy runs at 5.2), save 23 and load 19 us at 16384 x 2048
+// (4.4 and 5.4 TB/s). Fewer VALU operations (med3 clamps) change nothing. The group's
 // amax is a max of the bf16 magnitudes as integers (two per instruction, and a
 // NaN or infinity is simply the largest), then a butterfly over the group's
 // lanes.

@@ -24,6 +24,12 @@
 // contraction order is permuted, alike for both operands: a wave's load covers
 // 16 rows x 64 contiguous bytes.
 //
+// Measured at 128 experts, H 2048, F 768, top 8 (gate_up + down, us; the bytes of
+// the named experts): NVFP4, 1 token 13.5 + 5.4 (21 MB, latency); 64 tokens 62 + 47
+// (226 + 109 MB: 3.7 and 2.3 TB/s); FP8, 16 tokens 52 + 32 (260 + 130 MB: 5.0 and
+// 4.1 TB/s); INT4 with bf16 activations, 7 tokens 38 + 20. A 1 GiB device copy runs
+// at 5.2 TB/s.
+//
 // Sums are taken in a fixed order (no float atomics): the same call gives the
 // same bits. A token that names an expert twice counts as one pair with the
 // summed weight.
@@ -502,7 +508,9 @@ __device__ __forceinline__ int a_index(int seg, int f) {
 // expert's tokens once and streams the weights of several items past them. Its
 // eight waves are MT channel groups (gate and up rows of the same 16 channels)
 // times 8 / MT shares of the contraction. The first weights of an item are
-// requested before the sums of the one before are added up.
+// requested before the sums of the one before are added up. (One block per item
+// with a plan and staging of its own took 98 us where this takes 62: 64 tokens,
+// NVFP4; its streaming phase then runs at 6 TB/s behind a start of 12 us.)
 template <int FMT, int MODE, bool F16, bool WHOLE, int MT>
 __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
   constexpr int kChunk = Fmt<FMT>::kChunk, kSeg = Fmt<FMT>::kSeg, kSteps = Fmt<FMT>::kSteps;
@@ -815,7 +823,10 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
 // the result are used (the MFMAs have time to spare, the weights are decoded
 // once either way). A wave takes units (two experts, part of the contraction)
 // in turn and adds their weighted sums to its own [T, 8] block in LDS; the
-// waves' blocks are added in wave order.
+// waves' blocks are added in wave order. (Splitting the experts over blocks, the
+// last one adding the parts, cost 40 us in device-wide fences alone.) A wave's
+// loads return in order, so a batch waits for its A rows behind the weights
+// requested for the next one: about 4 us a batch with 4 tokens per expert.
 template <int FMT, int MODE, bool F16, bool WHOLE>
 __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
   constexpr int kChunk = Fmt<FMT>::kChunk, kSeg = Fmt<FMT>::kSeg, kSteps = Fmt<FMT>::kSteps;
