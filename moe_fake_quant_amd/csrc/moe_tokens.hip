@@ -13,12 +13,12 @@
 // point, E2M1 times its E4M3 block scale: at most 8 significant bits) is a
 // bf16 number, and so is an activation's; the fp32 scales that are constant
 // over a contraction (per channel, per tensor, per 128-group, the NVFP4 tensor
-// scale, s_a) multiply the fp32 sums instead. Only weight groups smaller than
-// a chunk (see Fmt) fold their scale into the operand, which rounds it to the
+// scale, s_a) multiply the fp32 sums instead. Only weight groups that are no
+// multiple of a chunk (see Fmt) fold their scale into the operand, which rounds it to the
 // bf16 value the training forward uses, and A without an activation format is
 // stored as bf16, as in the training forward. h stays in fp32.
 //
-// Contraction: v_mfma_f32_16x16x32_bf16 with 16 weight rows as the row operand
+// Contraction: v_mfma_f32_16x16x32 (bf16, or f16: see mfma_step) with 16 weight rows as the row operand
 // and up to 16 tokens as columns. A lane loads 16 bytes of codes of its row
 // at once (32 four-bit codes) and feeds them to consecutive MFMAs, so the
 // contraction order is permuted, alike for both operands: a wave's load covers
@@ -54,7 +54,7 @@ constexpr int kWavesD = kNTd / 64;
 enum ScaleMode {
   kEnd = 0,   // constant along the row (per channel / per tensor, or none): the finished sum
   kPost = 1,  // group a multiple of a chunk: the chunk's sum
-  kPre = 2    // smaller groups, NVFP4's E4M3 block scale: the operand
+  kPre = 2    // other groups, NVFP4's E4M3 block scale: the operand
 };
 
 // Codes a lane takes from one 16-byte load (kSeg), and the chunk of the
@@ -85,9 +85,9 @@ struct TokStack {  // one projection's stored weights
 
 // The scales of an item's rows pass through LDS: the rows of a tile lie behind
 // one another, so they are fetched in whole cache lines, where a load per lane
-// and segment would touch 16 lines for a few bytes of each (and took as long as
-// the load of the segment's codes). A row's bytes, and its distance in LDS
-// (8 more, so that a column of rows falls into different banks).
+// and segment would touch 16 lines for a few bytes of each. A row's bytes, and
+// its distance in LDS (8 more, so that a column of rows falls into different
+// banks).
 struct RowBytes {
   int n, stride;
   FastDiv per8, per1;  // / 8-byte units, / bytes of a row
