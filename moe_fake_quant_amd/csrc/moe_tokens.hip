@@ -120,7 +120,7 @@ struct TokArgs {
   RowBytes rsc, rzp;        // gate_up: scale (or scale byte) and zero point bytes of a row
   int agroups, arow;        // A's 16-channel groups and row length, padded to whole chunks
   // workspace. Rows are the pairs in expert order.
-  uint16_t *a;              // [P, arow] A's grid values, in MFMA step order (see a_index)
+  uint16_t *a;              // [P, arow] A's grid values, expert by expert (see a_offset)
   int4 *act;                // [min(P, E)] the experts with rows: {expert, first row, rows, 0}
   int32_t *nact;            // their number
   int32_t *tok;             // [P] a row's token
@@ -491,16 +491,20 @@ __device__ __forceinline__ bf16x8_t stage_vec(const ActQ &q, bf16x8_t o, float r
   return o;
 }
 
-// Where channel f of A lies in its row: within a chunk of the down projection
-// the elements of one MFMA step are contiguous (step, lane group, 8 elements),
-// so that a step's operand is read in whole 64-byte pieces.
+// A's order. Channel f of a row comes at a_index(f): within a chunk of the down
+// projection the 32 elements of one MFMA step (4 lane groups x 8) are contiguous.
+// Such a piece of 64 bytes lies beside the same piece of the expert's other rows
+// (element i of piece p of row r: (p * rows + r) * 32 + i), so that a step's
+// operand is one contiguous stretch of rows * 64 bytes: a load's time goes with
+// the cache lines it touches.
 template <int SEG>
 __device__ __forceinline__ int a_index(int f) {
   const int in = f & (4 * SEG - 1);
   return (f - in) + (in & (SEG - 1)) / 8 * 32 + in / SEG * 8 + (in & 7);
 }
-__device__ __forceinline__ int a_index(int seg, int f) {
-  return seg == 32 ? a_index<32>(f) : seg == 16 ? a_index<16>(f) : f;
+__device__ __forceinline__ size_t a_offset(int seg, int f, int row, int rows) {
+  const int i = seg == 32 ? a_index<32>(f) : seg == 16 ? a_index<16>(f) : f;
+  return ((size_t)(i >> 5) * rows + row) * 32 + (i & 31);
 }
 
 // An item is MT x 16 channels of A for one expert and its tokens; a block takes
@@ -806,7 +810,7 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
                              : f32_to_bf16(av[0]);
         if (g * kTile >= a.F) v = 0u;
         if (c < nc)
-          a.a[(size_t)(off + c0 + c) * a.arow + a_index(a.d.seg, g * kTile + f)] = (uint16_t)v;
+          a.a[(size_t)off * a.arow + a_offset(a.d.seg, g * kTile + f, c0 + c, n)] = (uint16_t)v;
       }
       lds_barrier();
     }
@@ -928,7 +932,7 @@ __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
   auto step = [&](Batch &r, Batch &rn, At &t) {
     const int4 ac = act[(col >> 3) ? t.i1 : t.i0], ar = act[(kq >> 1) ? t.i1 : t.i0];
     // a column past the expert's last repeats it, and is not used
-    const int row_a = ac.y + min(t.c0 + (col & 7), ac.z - 1);
+    const int row_e = min(t.c0 + (col & 7), ac.z - 1), row_a = ac.y + row_e;
     if (t.cb == t.ch0) {
       const size_t row_r = (size_t)ar.x * w.N + n0 + 4 * (kq & 1);
       acc = {0, 0, 0, 0};
@@ -937,7 +941,8 @@ __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) rs[i] = row_scale<FMT, MODE>(w, ar.x, row_r + i);
     }
-    const uint16_t *ap = a.a + (size_t)row_a * a.arow + t.cb * kChunk + kq * 8;
+    const uint16_t *ap = a.a + (size_t)ac.y * a.arow + row_e * 32 + kq * 8;
+    const int piece = ac.z * 32;  // elements from a step to the next
     bf16x8_t b[kB][kSteps];
     auto load_b = [&](int i0) {
 #pragma unroll
@@ -945,7 +950,8 @@ __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
         if (t.cb + i0 + i < t.ch1) {
 #pragma unroll
           for (int st = 0; st < kSteps; ++st)
-            b[i][st] = *reinterpret_cast<const bf16x8_t *>(ap + (i0 + i) * kChunk + st * 32);
+            b[i][st] = *reinterpret_cast<const bf16x8_t *>(
+                ap + (uint32_t)(((t.cb + i0 + i) * kSteps + st) * piece));
         }
     };
     load_b(0);
