@@ -25,9 +25,9 @@
 // 16 rows x 64 contiguous bytes.
 //
 // Measured at 128 experts, H 2048, F 768, top 8 (gate_up + down, us; the bytes of
-// the named experts): NVFP4, 1 token 13.5 + 5.4 (21 MB, latency); 64 tokens 62 + 47
-// (226 + 109 MB: 3.7 and 2.3 TB/s); FP8, 16 tokens 52 + 32 (260 + 130 MB: 5.0 and
-// 4.1 TB/s); INT4 with bf16 activations, 7 tokens 38 + 20. A 1 GiB device copy runs
+// the named experts): NVFP4, 1 token 13.5 + 5.5 (21 MB, latency); 64 tokens 62 + 40
+// (226 + 109 MB: 3.7 and 2.7 TB/s); FP8, 16 tokens 52 + 31 (260 + 130 MB: 5.0 and
+// 4.2 TB/s); INT4 with bf16 activations, 7 tokens 38 + 20. A 1 GiB device copy runs
 // at 5.2 TB/s.
 //
 // Sums are taken in a fixed order (no float atomics): the same call gives the
@@ -828,9 +828,9 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
 // once either way). A wave takes units (two experts, part of the contraction)
 // in turn and adds their weighted sums to its own [T, 8] block in LDS; the
 // waves' blocks are added in wave order. (Splitting the experts over blocks, the
-// last one adding the parts, cost 40 us in device-wide fences alone.) A wave's
-// loads return in order, so a batch waits for its A rows behind the weights
-// requested for the next one: about 4 us a batch with 4 tokens per expert.
+// last one adding the parts, cost 40 us in device-wide fences alone.) Bound by its
+// gather loads: 64 tokens took 47 us with A row by row, 34 without the A loads, 33
+// without the weight loads, and 40 with A in its present order.
 template <int FMT, int MODE, bool F16, bool WHOLE>
 __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
   constexpr int kChunk = Fmt<FMT>::kChunk, kSeg = Fmt<FMT>::kSeg, kSteps = Fmt<FMT>::kSteps;
