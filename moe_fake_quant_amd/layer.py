@@ -382,8 +382,11 @@ class MoEFakeQuantLayer:
         if getattr(self, "stored", None) is None:
             raise ValueError("forward_tokens needs export() first")
         T = x.shape[0]
-        if expert_ids.shape != (T, self.topk) or probs.shape != (T, self.topk):
-            raise ValueError(f"expert_ids and probs must be [{T}, {self.topk}]")
+        if x.shape != (T, self.H) or x.dtype != torch.bfloat16:
+            raise ValueError(f"x must be bf16 [T, {self.H}]")
+        for name, t, dt in (("expert_ids", expert_ids, torch.int32), ("probs", probs, torch.float32)):
+            if t.shape != (T, self.topk) or t.dtype != dt:
+                raise ValueError(f"{name} must be {dt} [{T}, {self.topk}]")
         out = self.tok_out[:T]
         fq_moe_tokens(x, T, self.H, self.F, expert_ids, probs, self.topk, self.expert_begin,
                       self.E, *self.stored, self.aq1, self.aq2, out, self.tok_ws)

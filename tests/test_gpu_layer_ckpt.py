@@ -151,8 +151,11 @@ def test_export_and_decode(name, wfmt, afmt, group):
                                 *vals, afmt, np.float32(s1), np.float32(s2))
         err = np.abs(bf16_vals(host_bits(out)) - ref)
         assert np.all(err <= tol + 2.0 ** -8 * (np.abs(ref) + tol)), (name, T)
-    with pytest.raises(ValueError):
-        layer.forward_tokens(x[:4], ids[:3], p[:4])
+    for bad in ((x[:4], ids[:3], p[:4]), (x[:4], ids[:4], p[:4].half()),
+                (x[:4], ids[:4].long(), p[:4]), (x[:4, :128], ids[:4], p[:4]),
+                (x[:4].float(), ids[:4], p[:4])):
+        with pytest.raises(ValueError):
+            layer.forward_tokens(*bad)
     with pytest.raises(F.FQError):
         layer.forward_tokens(x.repeat(2, 1), ids.repeat(2, 1), p.repeat(2, 1))
 

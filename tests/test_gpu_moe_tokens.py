@@ -119,6 +119,23 @@ def test_every_token_on_one_expert():
     call.check()
 
 
+@pytest.mark.parametrize("fmt,group,afmt", [(O.FMT_NVFP4, 16, O.FMT_NVFP4),
+                                            (O.FMT_INT4, 128, O.FMT_NONE)])
+def test_hot_expert_among_others(fmt, group, afmt):
+    """Most tokens share one expert (several passes of columns), the rest name
+    others: the blocks' shares fall inside experts of different weight."""
+    c = make(seed=57, T=100, E=40, H=1024, F=256, topk=3, fmt=fmt, group=group, afmt=afmt)
+    c["ids"][:90, 1] = 17
+    c["ids"][90:, 2] = 39
+    call = Call(c)
+    call.run()
+    call.check()
+    first = call.out.clone()
+    call.ws.fill_(0xFF)              # nothing is kept in the workspace
+    call.run()
+    assert torch.equal(call.out, first)
+
+
 def test_wide_rows_stage_few_columns():
     """A row so wide that fewer than 16 token rows fit into LDS at a time."""
     run_case(seed=51, T=9, E=2, H=8192, F=32, topk=1, fmt=O.FMT_FP8, group=None, afmt=O.FMT_FP8)
