@@ -472,7 +472,7 @@ fq_status fq_moe_unpermute_reduce(const uint16_t *dxq_bf16, const int32_t *row_o
  * that the batch names are read (mcore_qad article, section 三: the formats'
  * stored layouts are the deployment side's; QAT + ZeRO-3 page, convert).
  *   h      = W_gu[e] . FQ_a1(x[t])                 [2F], gate first, fp32
- *   A      = FQ_a2(silu(h[:F]) * h[F:])            bf16 when aq2 is NONE
+ *   A      = FQ_a2(silu(h[:F]) * h[F:])            within 2^-16 of it when aq2 is NONE
  *   out[t] = bf16(sum_j probs[t,j] * W_d[e_tj] . A)
  *   over the slots j whose expert lies in [expert_begin, expert_begin +
  *   E_local); a token without such a slot gets 0. A token may name an expert

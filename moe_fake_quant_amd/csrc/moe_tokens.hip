@@ -15,10 +15,14 @@
 // over a contraction (per channel, per tensor, per 128-group, the NVFP4 tensor
 // scale, s_a) multiply the fp32 sums instead. Only weight groups that are no
 // multiple of a chunk (see Fmt) fold their scale into the operand, which rounds it to the
-// bf16 value the training forward uses, and A without an activation format is
-// stored as bf16, as in the training forward. h stays in fp32.
+// bf16 value the training forward uses. h stays in fp32. A without an activation
+// format is no grid value: it goes on as two bf16 numbers, A rounded and what that
+// leaves, each multiplied with the same weight operand. Together they are within
+// 2^-16 of A (half a bf16 step of half a bf16 step), so that the rounding of the
+// output is the only one that counts: against float64 the output is off by 0.0017
+// of its largest value, as with fp32 operands, where one bf16 A gives 0.0024.
 //
-// Contraction: v_mfma_f32_16x16x32 (bf16, or f16: see mfma_step) with 16 weight rows as the row operand
+// Contraction: v_mfma_f32_16x16x32 (bf16, or f16: see operand) with 16 weight rows as the row operand
 // and up to 16 tokens as columns. A lane loads 16 bytes of codes of its row
 // at once (32 four-bit codes) and feeds them to consecutive MFMAs, so the
 // contraction order is permuted, alike for both operands: a wave's load covers
@@ -79,6 +83,7 @@ struct TokStack {  // one projection's stored weights
   int nch;                  // chunks per row
   int whole;                // rows are whole chunks
   int f16;                  // operands are f16 (NVFP4 with quantized activations)
+  int parts;                // bf16 numbers to an activation: 2 for A without a format, else 1
   int seg;                  // Fmt::kSeg
   FastDiv dgroup;           // / group
 };
@@ -120,7 +125,7 @@ struct TokArgs {
   RowBytes rsc, rzp;        // gate_up: scale (or scale byte) and zero point bytes of a row
   int agroups, arow;        // A's 16-channel groups and row length, padded to whole chunks
   // workspace. Rows are the pairs in expert order.
-  uint16_t *a;              // [P, arow] A's grid values, expert by expert (see a_offset)
+  uint16_t *a;              // [P, arow, parts] A's grid values, expert by expert (see a_offset)
   int4 *act;                // [min(P, E)] the experts with rows: {expert, first row, rows, 0}
   int32_t *nact;            // their number
   int32_t *tok;             // [P] a row's token
@@ -185,8 +190,8 @@ struct Has {
   static constexpr bool kZp = FMT == FQ_FMT_INT4;
 };
 
-// One MFMA over step st of a chunk: 8 consecutive elements of the lane's row
-// against the 8 activation grid values in x (bf16, or f16 with F16).
+// The row operand of one MFMA, step st of a chunk: 8 consecutive elements of the
+// lane's row as grid values (bf16, or f16 with F16).
 //
 // VALU operations per 8 codes: E4M3 4 (the converter makes bf16 pairs), NVFP4
 // 8 in f16 (convert and multiply pairs by the block scale) or 16 through fp32
@@ -194,8 +199,7 @@ struct Has {
 // value exactly (at most 8 bits, 2^-10 <= |v| <= 2688), but not any bf16
 // activation, so it is used for quantized activations.
 template <int FMT, int MODE, bool F16>
-__device__ __forceinline__ f32x4 mfma_step(const Codes &r, const Scales &q, int st,
-                                           const bf16x8_t &x, f32x4 acc) {
+__device__ __forceinline__ bf16x8_t operand(const Codes &r, const Scales &q, int st) {
   if (FMT == FQ_FMT_NVFP4 && F16) {
     const uint32_t c = r.w[st];
     const f16x2 th = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q.sb, 1.0f, false);
@@ -206,8 +210,7 @@ __device__ __forceinline__ f32x4 mfma_step(const Codes &r, const Scales &q, int 
     v[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 1) * ss;
     v[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 2) * ss;
     v[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 3) * ss;
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8v, v),
-                                                  __builtin_bit_cast(f16x8v, x), acc, 0, 0, 0);
+    return __builtin_bit_cast(bf16x8_t, v);
   }
   bf16x8_t o;
   if (FMT == FQ_FMT_NONE) {
@@ -261,6 +264,15 @@ __device__ __forceinline__ f32x4 mfma_step(const Codes &r, const Scales &q, int 
     }
     o = pack8(v);
   }
+  return o;
+}
+
+// acc plus the products of a row operand and 8 activation values of its type
+template <bool F16>
+__device__ __forceinline__ f32x4 mfma(const bf16x8_t &o, const bf16x8_t &x, f32x4 acc) {
+  if (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8v, o),
+                                                  __builtin_bit_cast(f16x8v, x), acc, 0, 0, 0);
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8v, o),
                                                  __builtin_bit_cast(bf16x8v, x), acc, 0, 0, 0);
 }
@@ -308,6 +320,7 @@ __device__ __forceinline__ void act_grid(const ActQ &q, float theta, float *x) {
 
 // ---------------------------------------------------------------- gate_up ---
 constexpr int kTile = 16;                        // A channels of one wave's pair of tiles
+constexpr float kBf16Max = 0x1.FEp127f;
 constexpr int kRedBytes = kWaves * 2 * 64 * 16;  // the waves' sums of their two tiles
 
 // bytes of one staged token row: the row padded to whole chunks, and 16 more
@@ -496,15 +509,16 @@ __device__ __forceinline__ bf16x8_t stage_vec(const ActQ &q, bf16x8_t o, float r
 // Such a piece of 64 bytes lies beside the same piece of the expert's other rows
 // (element i of piece p of row r: (p * rows + r) * 32 + i), so that a step's
 // operand is one contiguous stretch of rows * 64 bytes: a load's time goes with
-// the cache lines it touches.
+// the cache lines it touches. With two parts to an element, a row's piece is its
+// 32 rounded values and behind them the 32 rests.
 template <int SEG>
 __device__ __forceinline__ int a_index(int f) {
   const int in = f & (4 * SEG - 1);
   return (f - in) + (in & (SEG - 1)) / 8 * 32 + in / SEG * 8 + (in & 7);
 }
-__device__ __forceinline__ size_t a_offset(int seg, int f, int row, int rows) {
+__device__ __forceinline__ size_t a_offset(int seg, int parts, int f, int row, int rows) {
   const int i = seg == 32 ? a_index<32>(f) : seg == 16 ? a_index<16>(f) : f;
-  return ((size_t)(i >> 5) * rows + row) * 32 + (i & 31);
+  return ((size_t)(i >> 5) * rows + row) * (32 * parts) + (i & 31);
 }
 
 // An item is MT x 16 channels of A for one expert and its tokens; a block takes
@@ -735,8 +749,8 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
           for (int st = 0; st < kSteps; ++st) {
             const bf16x8_t b =
                 *reinterpret_cast<const bf16x8_t *>(xs + (ch * kChunk + st * 8) * 2);
-            s0 = mfma_step<FMT, MODE, F16>(r[u][0], qg, st, b, s0);
-            s1 = mfma_step<FMT, MODE, F16>(r[u][1], qu, st, b, s1);
+            s0 = mfma<F16>(operand<FMT, MODE, F16>(r[u][0], qg, st), b, s0);
+            s1 = mfma<F16>(operand<FMT, MODE, F16>(r[u][1], qu, st), b, s1);
           }
           if (MODE == kPost) {
             acc[0] += s0 * chunk_scales(rg, ch);
@@ -807,10 +821,16 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
         }
         act_grid<2>(q2, theta, av);
         uint32_t v = a.d.f16 ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(av[0], 0.0f))
-                             : f32_to_bf16(av[0]);
-        if (g * kTile >= a.F) v = 0u;
-        if (c < nc)
-          a.a[(size_t)off * a.arow + a_offset(a.d.seg, g * kTile + f, c0 + c, n)] = (uint16_t)v;
+                             : f32_to_bf16(fminf(fmaxf(av[0], -kBf16Max), kBf16Max));
+        // what v leaves of A (a NaN or infinity: itself)
+        uint32_t rest = f32_to_bf16(av[0] - bf16_to_f32(v));
+        if (g * kTile >= a.F) v = rest = 0u;
+        if (c < nc) {
+          uint16_t *to = a.a + (size_t)off * a.arow * a.d.parts +
+                         a_offset(a.d.seg, a.d.parts, g * kTile + f, c0 + c, n);
+          to[0] = (uint16_t)v;
+          if (a.d.parts == 2) to[32] = (uint16_t)rest;
+        }
       }
       lds_barrier();
     }
@@ -831,12 +851,13 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
 // last one adding the parts, cost 40 us in device-wide fences alone.) Bound by its
 // gather loads: 64 tokens took 47 us with A row by row, 34 without the A loads, 33
 // without the weight loads, and 40 with A in its present order.
-template <int FMT, int MODE, bool F16, bool WHOLE>
+template <int FMT, int MODE, bool F16, bool WHOLE, int PARTS>
 __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
   constexpr int kChunk = Fmt<FMT>::kChunk, kSeg = Fmt<FMT>::kSeg, kSteps = Fmt<FMT>::kSteps;
   constexpr bool kSb = Has<FMT, MODE>::kSb, kS = Has<FMT, MODE>::kS, kZp = Has<FMT, MODE>::kZp;
   constexpr int kU = 4;                        // chunks whose codes are requested together
-  constexpr int kB = Fmt<FMT>::k4bit ? 2 : 4;  // chunks whose activations are
+  // chunks whose activations are: 32 registers of them
+  constexpr int kB = FMT == FQ_FMT_NONE ? 4 : (Fmt<FMT>::k4bit ? 2 : 4) / PARTS;
   __shared__ int4 act[1024];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -941,17 +962,19 @@ __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) rs[i] = row_scale<FMT, MODE>(w, ar.x, row_r + i);
     }
-    const uint16_t *ap = a.a + (size_t)ac.y * a.arow + row_e * 32 + kq * 8;
-    const int piece = ac.z * 32;  // elements from a step to the next
-    bf16x8_t b[kB][kSteps];
+    const uint16_t *ap = a.a + ((size_t)ac.y * a.arow + row_e * 32) * PARTS + kq * 8;
+    const int piece = ac.z * 32 * PARTS;  // elements from a step to the next
+    bf16x8_t b[kB][kSteps][PARTS];
     auto load_b = [&](int i0) {
 #pragma unroll
       for (int i = 0; i < kB; ++i)
         if (t.cb + i0 + i < t.ch1) {
 #pragma unroll
           for (int st = 0; st < kSteps; ++st)
-            b[i][st] = *reinterpret_cast<const bf16x8_t *>(
-                ap + (uint32_t)(((t.cb + i0 + i) * kSteps + st) * piece));
+#pragma unroll
+            for (int h = 0; h < PARTS; ++h)
+              b[i][st][h] = *reinterpret_cast<const bf16x8_t *>(
+                  ap + (uint32_t)(((t.cb + i0 + i) * kSteps + st) * piece) + h * 32);
         }
     };
     load_b(0);
@@ -977,8 +1000,11 @@ __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
       f32x4 s = {0, 0, 0, 0};
       if (MODE != kPost) s = acc;
 #pragma unroll
-      for (int st = 0; st < kSteps; ++st)
-        s = mfma_step<FMT, MODE, F16>(r.c[i], q, st, b[i % kB][st], s);
+      for (int st = 0; st < kSteps; ++st) {
+        const bf16x8_t o = operand<FMT, MODE, F16>(r.c[i], q, st);
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h) s = mfma<F16>(o, b[i % kB][st][h], s);
+      }
       if (MODE == kPost) {
         // weight row 4 kq + i of the result is lane 4 kq + i's row
 #pragma unroll
@@ -1051,6 +1077,7 @@ TokStack tok_stack(const fq_stored_w &w, int N, int K, int afmt) {
   t.whole = K % chunk == 0;
   t.seg = chunk / 4;
   t.f16 = w.fmt == FQ_FMT_NVFP4 && afmt != FQ_FMT_NONE;
+  t.parts = afmt == FQ_FMT_NONE ? 2 : 1;
   t.dgroup = FastDiv((uint32_t)group);
   return t;
 }
@@ -1066,7 +1093,14 @@ struct Launch {
 
 template <int FMT, int MODE, bool F16, bool WHOLE>
 void launch_down(const Launch &l, const TokArgs &a, hipStream_t st) {
-  hipLaunchKernelGGL((k_tok_down<FMT, MODE, F16, WHOLE>), l.grid, dim3(kNTd), l.lds, st, a);
+  // NVFP4 goes through f16 with an activation format and through bf16 without
+  constexpr bool kOne = F16 || FMT != FQ_FMT_NVFP4, kTwo = !F16;
+  if constexpr (kOne)
+    if (a.d.parts == 1)
+      hipLaunchKernelGGL((k_tok_down<FMT, MODE, F16, WHOLE, 1>), l.grid, dim3(kNTd), l.lds, st, a);
+  if constexpr (kTwo)
+    if (a.d.parts == 2)
+      hipLaunchKernelGGL((k_tok_down<FMT, MODE, F16, WHOLE, 2>), l.grid, dim3(kNTd), l.lds, st, a);
 }
 template <int FMT, int MODE, bool F16, bool WHOLE, int MT>
 void launch_gate_up(const Launch &l, const TokArgs &a, hipStream_t st) {
@@ -1117,7 +1151,7 @@ TokWs tok_ws(int T, int topk, int E, int F) {
   const size_t P = (size_t)T * topk, slots = P < (size_t)E ? P : (size_t)E;
   TokWs w;
   size_t o = 0;
-  w.a = o;     o += up256(P * arow * 2);
+  w.a = o;     o += up256(P * arow * 2 * 2);  // two parts to an element at most
   w.act = o;   o += up256(slots * 16);
   w.nact = o;  o += 256;
   w.tok = o;   o += up256(P * 4);

@@ -2,13 +2,16 @@
 infrastructure only): float64 from the definition, with a bound on what fp32
 arithmetic may change.
 
-h = W_gu FQ_a1(x), a = silu(h_g) h_u in full precision, A = FQ_a2(a) (bf16
+h = W_gu FQ_a1(x), a = silu(h_g) h_u in full precision, A = FQ_a2(a) (a itself
 without an activation format), out[t] = sum over the local slots of p W_d A.
 
 The bound: an fp32 sum of n products in any order is off by at most
 (n + 32) 2^-24 times the sum of the magnitudes; that moves a, and the
 quantizer maps the moved interval onto grid values (an interval that crosses a
-rounding border takes the values of both sides).
+rounding border takes the values of both sides). Without an activation format
+the other side may hold A as two bf16 numbers, A rounded (off by at most half a
+step, 2^-8 |A|) and the rest rounded (2^-8 of that): 2^-16 |A| in all, or half
+the smallest subnormal step, and a sum of twice as many products.
 """
 from __future__ import annotations
 
@@ -17,7 +20,7 @@ import numpy as np
 from .codecs import (FMT_FP8, FMT_INT4, FMT_INT8, FMT_NONE, FMT_NVFP4, E2M1_MAX, E4M3_MAX,
                      e2m1_round, e4m3_round, fq_act, fq_weight_stack)
 from .moe import _sigmoid
-from .numerics import bf16_to_f32, f64_to_bf16
+from .numerics import bf16_to_f32
 
 U = 2.0 ** -24
 
@@ -47,8 +50,6 @@ def _quant(a, fmt, s, theta=None):
     """FQ_a of fp32 rows on a given NVFP4 theta (else its own), float64 values."""
     a = np.asarray(a, np.float32)
     s = np.float32(s)
-    if fmt == FMT_NONE:
-        return bf16_to_f32(f64_to_bf16(a)).astype(np.float64)
     if fmt == FMT_NVFP4:
         sb = (theta * s).astype(np.float32)
         with np.errstate(divide="ignore", invalid="ignore"):
@@ -70,6 +71,8 @@ def _theta(amax, s):
 def quant_interval(lo, mid, hi, fmt, s):
     """FQ_a(mid) and the largest distance from it that a value between lo and
     hi (elementwise) may be quantized to."""
+    if fmt == FMT_NONE:
+        return mid, np.maximum(hi - mid, mid - lo) + 2.0 ** -16 * np.abs(mid) + 2.0 ** -134
     if fmt != FMT_NVFP4:
         v = _quant(mid, fmt, s)
         return v, np.maximum(np.abs(_quant(lo, fmt, s) - v), np.abs(_quant(hi, fmt, s) - v))
@@ -115,6 +118,7 @@ def moe_tokens(x_bits, ids, probs, ebegin: int, w_gu, w_d, afmt: int, s1, s2, re
             A, dA = A[0], dA[0] + 4 * U * np.abs(A[0])
             o = w_d[e] @ A
             mag = np.abs(w_d[e]) @ np.abs(A)
+            n = 2 * F if afmt == FMT_NONE else F
             out[t] += p * o
-            tol[t] += abs(p) * (np.abs(w_d[e]) @ dA + (F + 36) * U * mag + rel_h * np.abs(o))
+            tol[t] += abs(p) * (np.abs(w_d[e]) @ dA + (n + 36) * U * mag + rel_h * np.abs(o))
     return out, tol + 80 * U * np.abs(out)
