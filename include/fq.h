@@ -489,9 +489,13 @@ fq_status fq_moe_unpermute_reduce(const uint16_t *dxq_bf16, const int32_t *row_o
  * x_bf16, out_bf16 [T, H]; expert_ids, probs [T, topk]. out must not overlap x.
  * codes and the scale pointers 16-byte aligned (global_scale: 4-byte).
  * 0 <= T <= 128 (for more tokens the grouped GEMM calls are the path),
- * 1 <= topk <= 64, E_local <= 1024, H and F % 16 == 0 and <= 16384. Very wide
- * rows of small int8 / fp8 / int4 groups whose scales do not fit into LDS (16
- * rows times H/group fp32 scales, near H = 16384) are FQ_ERR_UNSUPPORTED.
+ * 1 <= topk <= 64, E_local <= 1024, H and F % 16 == 0 and <= 16384. The scales
+ * of 32 rows of w_gu lie in LDS beside a token row: where small int8 / fp8
+ * groups make
+ *   32 * (up8(4 * H/group) + 8) + 2 * H + 16 + up16(2 * T * topk) + 11884
+ * more than 163840 (up8, up16: rounded up to a multiple; H up to whole 64s), the
+ * call is FQ_ERR_UNSUPPORTED: groups of 16 above H = 15136 for up to 96 pairs
+ * T * topk, above H = 13504 for any number. int4 groups always fit.
  * Workspace: fq_workspace_bytes(FQ_OP_MOE_TOKENS, {E_local, H, F}, T * topk,
  * topk). Calls that may overlap on the device need workspaces of their own
  * (two graphs captured over one workspace must not be replayed at once).

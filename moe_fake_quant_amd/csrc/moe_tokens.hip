@@ -1082,7 +1082,11 @@ TokStack tok_stack(const fq_stored_w &w, int N, int K, int afmt) {
   return t;
 }
 
-constexpr int kMtTail = 2;  // channel groups per gate_up item where rows end inside a chunk
+// channel groups per gate_up item where rows end inside a chunk: this many, or one
+// where the scales of its 64 rows do not fit into LDS
+constexpr int kMtTail = 2;
+constexpr int kLdsBytes = 160 << 10;
+constexpr int kPlanBytes = 14 << 10;  // room left for the plan
 
 struct Launch {
   bool down;
@@ -1112,7 +1116,12 @@ void launch_one(const Launch &l, const TokArgs &a, hipStream_t st) {
   // groups of whole chunks make rows of whole chunks
   if constexpr (MODE != kPost) {
     if (l.down && !a.d.whole) return launch_down<FMT, MODE, F16, false>(l, a, st);
-    if (!l.down && !a.gu.whole) return launch_gate_up<FMT, MODE, F16, false, kMtTail>(l, a, st);
+    if (!l.down && !a.gu.whole) {
+      // only these have rows of so many scale bytes
+      if constexpr (MODE == kPre && FMT != FQ_FMT_NVFP4)
+        if (l.mt == 1) return launch_gate_up<FMT, MODE, F16, false, 1>(l, a, st);
+      return launch_gate_up<FMT, MODE, F16, false, kMtTail>(l, a, st);
+    }
   }
   if (l.down) launch_down<FMT, MODE, F16, true>(l, a, st);
   else if (l.mt == 4) launch_gate_up<FMT, MODE, F16, true, 4>(l, a, st);
@@ -1180,16 +1189,17 @@ Launch gate_up_launch(TokArgs &a, const fq_stored_w &w_gu) {
   a.rzp = row_bytes(f == FQ_FMT_INT4 ? ng : 0);
   const int per_row = (a.rsc.n ? a.rsc.stride : 0) + (a.rzp.n ? a.rzp.stride : 0);
   while (mt > 1 && 2 * mt * kTile * per_row > (20 << 10)) mt /= 2;
-  if (!a.gu.whole) mt = kMtTail;
+  const int chunk = a.gu.seg * 4, row = xrow_bytes(a.gu.K, chunk);
+  a.idb = (a.P * 2 + 15) / 16 * 16;
+  if (!a.gu.whole)
+    mt = 2 * kMtTail * kTile * per_row + row + a.idb + kPlanBytes <= kLdsBytes ? kMtTail : 1;
   a.ny = (a.agroups + mt - 1) / mt;
   a.dny = FastDiv((uint32_t)a.ny);
   // token rows staged at a time: 16 columns of an MFMA, or what leaves two
   // blocks to a CU (80 KB, 14 of them the plan), at least one
-  const int chunk = a.gu.seg * 4, row = xrow_bytes(a.gu.K, chunk);
   int sums = 2 * mt * kTile * per_row;
   if (sums < kRedBytes) sums = kRedBytes;
-  a.idb = (a.P * 2 + 15) / 16 * 16;
-  int nc = ((80 << 10) - (14 << 10) - a.idb - sums) / row;
+  int nc = ((80 << 10) - kPlanBytes - a.idb - sums) / row;
   nc = nc < 1 ? 1 : nc > 16 ? 16 : nc;
   a.ncol = nc < a.T ? nc : a.T;
   a.xb = a.ncol * row;

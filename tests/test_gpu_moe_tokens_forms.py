@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 import oracle as O
-from test_gpu_moe_tokens import Call, make
+from test_gpu_moe_tokens import Call, make, run_case
 from test_oracle_moe_tokens_a import FORMS, difference_case
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +45,13 @@ def test_a_beyond_the_largest_bf16_number():
     assert np.all(np.abs(got[0] - Fc * 2.0 ** -10 * a0) <= 2.0 ** -8 * Fc * 2.0 ** -10 * a0)
     assert np.all(np.isposinf(got[1]))
     assert np.all(np.abs(got[2] + Fc * 2.0 ** -10 * 256.0) <= 2.0 ** -8 * Fc * 0.25)
+
+
+@pytest.mark.parametrize("fmt,group,afmt,H", [(O.FMT_INT8, 16, O.FMT_INT8, 8400),
+                                              (O.FMT_FP8, 16, O.FMT_NONE, 15136),
+                                              (O.FMT_FP8, 16, O.FMT_FP8, 15104),
+                                              (O.FMT_INT4, 32, O.FMT_NONE, 16352)])
+def test_wide_rows_of_small_groups(fmt, group, afmt, H):
+    """Scale rows that fit into LDS for one channel group only, rows that end
+    inside a chunk and whole ones, up to the widest accepted."""
+    run_case(seed=110, T=3, E=2, H=H, F=32, topk=1, fmt=fmt, group=group, afmt=afmt)
