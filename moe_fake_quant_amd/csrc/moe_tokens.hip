@@ -1086,7 +1086,7 @@ TokStack tok_stack(const fq_stored_w &w, int N, int K, int afmt) {
 // where the scales of its 64 rows do not fit into LDS
 constexpr int kMtTail = 2;
 constexpr int kLdsBytes = 160 << 10;
-constexpr int kPlanBytes = 14 << 10;  // room left for the plan
+constexpr int kPlanBytes = sizeof(Plan) + 2 * 4 * kTile * sizeof(float);  // and the rows' factors
 
 struct Launch {
   bool down;
@@ -1196,10 +1196,10 @@ Launch gate_up_launch(TokArgs &a, const fq_stored_w &w_gu) {
   a.ny = (a.agroups + mt - 1) / mt;
   a.dny = FastDiv((uint32_t)a.ny);
   // token rows staged at a time: 16 columns of an MFMA, or what leaves two
-  // blocks to a CU (80 KB, 14 of them the plan), at least one
+  // blocks to a CU (80 KB, 11.6 of them the plan), at least one
   int sums = 2 * mt * kTile * per_row;
   if (sums < kRedBytes) sums = kRedBytes;
-  int nc = ((80 << 10) - kPlanBytes - a.idb - sums) / row;
+  int nc = (kLdsBytes / 2 - kPlanBytes - a.idb - sums) / row;
   nc = nc < 1 ? 1 : nc > 16 ? 16 : nc;
   a.ncol = nc < a.T ? nc : a.T;
   a.xb = a.ncol * row;
@@ -1234,7 +1234,7 @@ size_t moe_tokens_lds_bytes(int T, int H, int F, int topk, int E, const fq_store
                             const fq_stored_w &w_d) {
   TokArgs a{};
   set_sizes(a, T, H, F, topk, E, w_gu, w_d, FQ_FMT_NONE, FQ_FMT_NONE);
-  return (size_t)gate_up_launch(a, w_gu).lds + sizeof(Plan) + 2 * 4 * kTile * sizeof(float);
+  return (size_t)gate_up_launch(a, w_gu).lds + kPlanBytes;
 }
 
 void launch_moe_tokens(const uint16_t *x, int T, int H, int F, const int32_t *ids,
