@@ -79,7 +79,8 @@ class MoEFakeQuantLayer:
         ckpt (fmt, group): FMT_INT8 or FMT_FP8_E4M3 checkpoints of h and the
         input (group as in fq_ckpt_save, dividing F and H). scratch_of: another
         checkpointed layer of the same sizes and formats, on the same stream,
-        whose buffers this one shares: out and dx hold the last layer's."""
+        whose buffers this one shares: out and dx hold the last layer's, so that
+        a layer whose input was another's out takes None in its backward."""
         assert w_gu.dtype == torch.bfloat16 and w_d.dtype == torch.bfloat16
         self.dev = w_gu.device
         self.E, F2, self.H = w_gu.shape
@@ -173,6 +174,8 @@ class MoEFakeQuantLayer:
             self.side = torch.cuda.Stream(device=self.dev)   # default priority
             self.ev_do = torch.cuda.Event()
             self.ev_dh = torch.cuda.Event()
+        self._scratch_at = {t.untyped_storage().data_ptr() for t in (getattr(self, n) for n in _SCRATCH)
+                            if isinstance(t, torch.Tensor)}
         self.overlap_wgrad = True
         self.T = 0
 
@@ -285,10 +288,16 @@ class MoEFakeQuantLayer:
         return x
 
     def backward(self, x: Optional[torch.Tensor], probs: torch.Tensor, dout: torch.Tensor):
-        """x None (checkpointed layers): the input is taken from its checkpoint."""
+        """x None (checkpointed layers): the input is taken from its checkpoint.
+        An x in one of a checkpointed layer's buffers is refused: by now a forward
+        (its own, or of a layer that shares them) has written over it."""
         T = self.T if x is None else x.shape[0]
         if x is None and self.ckpt is None:
             raise ValueError("backward without x needs a checkpointed layer")
+        if self.ckpt is not None and x is not None \
+                and x.untyped_storage().data_ptr() in self._scratch_at:
+            raise ValueError("x lies in a buffer of the checkpointed layers that has been overwritten "
+                             "since the forward: pass None (the input's checkpoint), or a copy")
         main = torch.cuda.current_stream(self.dev)
         if self.overlap_wgrad:
             # the side stream's previous step (and anything else the caller
