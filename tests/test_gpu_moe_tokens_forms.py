@@ -6,6 +6,7 @@ import pytest
 import oracle as O
 from test_gpu_moe_tokens import Call, make, run_case
 from test_oracle_moe_tokens_a import FORMS, difference_case
+from tokens_case import reference
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +56,67 @@ def test_wide_rows_of_small_groups(fmt, group, afmt, H):
     """Scale rows that fit into LDS for one channel group only, rows that end
     inside a chunk and whole ones, up to the widest accepted."""
     run_case(seed=110, T=3, E=2, H=H, F=32, topk=1, fmt=fmt, group=group, afmt=afmt)
+
+
+def channel_groups(c):
+    """The channel groups of a gate_up item (whole rows), by the launch's rule."""
+    fmt, group = c["gu"][0], c["gu"][1]
+    chunk = {O.FMT_NONE: 32, O.FMT_INT8: 64, O.FMT_FP8: 64}.get(c["d"][0], 128)
+    groups = -(-c["F"] // chunk) * chunk // 16
+    slots = min(c["T"] * c["topk"], c["E"])
+    mt = 4
+    while mt > 1 and slots * -(-groups // mt) < 1024:
+        mt //= 2
+    ng = c["H"] // group if group > 0 else 0
+    up = lambda n: (n + 7) // 8 * 8 + 8  # noqa: E731
+    row = up(c["H"] // 16) if fmt == O.FMT_NVFP4 else up(4 * ng) if ng > 1 else 0
+    row += up(ng) if fmt == O.FMT_INT4 else 0
+    while mt > 1 and 2 * mt * 16 * row > 20480:
+        mt //= 2
+    return mt
+
+
+def tiled(c, times, ids):
+    """The call over `times` copies of the experts, expert e at e, e + E, ...:
+    a stack of many experts whose float64 form is that of a few."""
+    E = c["E"]
+    call = Call(dict(c, E=E * times, ids=ids))
+    for st in (call.gu, call.d):
+        for name in ("codes", "scale", "scale_bytes", "zero_point_bytes", "global_scale"):
+            t = getattr(st, name)
+            if t is not None:
+                setattr(st, name, t.reshape(E, -1).repeat(times, 1).reshape(-1))
+    return call, reference(dict(c, ids=ids % E))
+
+
+WIDE_ITEMS = [(O.FMT_NVFP4, 16, O.FMT_NVFP4, 1152), (O.FMT_NVFP4, 16, O.FMT_NONE, 1152),
+              (O.FMT_FP8, None, O.FMT_FP8, 1152), (O.FMT_FP8, O.GROUP_TENSOR, O.FMT_FP8, 1152),
+              (O.FMT_FP8, 64, O.FMT_NONE, 1152), (O.FMT_FP8, 16, O.FMT_FP8, 576),
+              (O.FMT_INT4, 128, O.FMT_NONE, 1152), (O.FMT_INT4, 32, O.FMT_FP8, 768),
+              (O.FMT_INT4, None, O.FMT_NONE, 1152), (O.FMT_INT8, None, O.FMT_INT8, 1152),
+              (O.FMT_INT8, 192, O.FMT_INT8, 1152), (O.FMT_INT8, 32, O.FMT_NONE, 1152),
+              (O.FMT_INT8, O.GROUP_TENSOR, O.FMT_INT8, 1152), (O.FMT_NONE, 0, O.FMT_NONE, 1152)]
+
+
+@pytest.mark.parametrize("fmt,group,afmt,H", WIDE_ITEMS)
+@pytest.mark.parametrize("mt", [4, 2])
+def test_items_of_several_channel_groups(fmt, group, afmt, H, mt):
+    """Enough experts for items of 64 and of 32 channels, F = 17 x 16 that ends
+    inside an item, contractions of several rounds of the waves, and an expert
+    of more rows than one pass stages."""
+    topk = 2 * mt
+    c = make(seed=120 + mt, T=32, E=8, H=H, F=272, topk=topk, fmt=fmt, group=group,
+             group_d=272 if group and group > 16 else None, afmt=afmt)
+    ids = np.stack([np.random.default_rng(t).permutation(256)[:topk] for t in range(32)])
+    ids[:20, 0] = 17
+    call, ref = tiled(c, 32, ids.astype(np.int32))
+    assert channel_groups(call.c) == mt
+    print(f"[tokens] {mt} channel groups fmt={fmt} group={group} afmt={afmt} H={H}", flush=True)
+    call.run()
+    call.check(ref)
+
+
+@pytest.mark.parametrize("fmt,afmt", [(O.FMT_FP8, O.FMT_FP8), (O.FMT_INT8, O.FMT_NONE)])
+def test_wide_rows_of_small_groups_two_channel_groups(fmt, afmt):
+    """Rows that end inside a chunk, 64 of them with their scales in LDS."""
+    run_case(seed=111, T=9, E=3, H=4112, F=48, topk=2, fmt=fmt, group=16, afmt=afmt)

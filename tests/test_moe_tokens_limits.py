@@ -1,6 +1,7 @@
 """Which rows of the few-token MoE layer fit into LDS: the documented sum, on
 both sides of it (no GPU needed: the workspace is checked after the size)."""
 import ctypes
+import os
 
 import pytest
 
@@ -60,3 +61,15 @@ def test_other_scale_modes_always_fit(pkg):  # noqa: F811
         for H in list(range(16, 2064, 16)) + list(range(14000, 16385, 16)):
             assert status(pkg.lib(), pkg, fmt, H, H if group is None else group, 128, 64) == \
                 pkg.FQ_ERR_WORKSPACE_TOO_SMALL, H
+
+
+def test_the_rule_for_channel_groups(repo_root):
+    """test_gpu_moe_tokens_forms chooses its sizes by a copy of the launch's rule:
+    whoever changes one changes the other."""
+    src = os.path.join(repo_root, "moe_fake_quant_amd", "csrc", "moe_tokens.hip")
+    with open(src) as f:
+        text = f.read()
+    for line in ("const int slots = a.P < a.E ? a.P : a.E;", "int mt = 4;",
+                 "while (mt > 1 && (long)slots * ((a.agroups + mt - 1) / mt) < 1024) mt /= 2;",
+                 "while (mt > 1 && 2 * mt * kTile * per_row > (20 << 10)) mt /= 2;"):
+        assert text.count(line) == 1, line
