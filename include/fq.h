@@ -478,9 +478,9 @@ fq_status fq_moe_unpermute_reduce(const uint16_t *dxq_bf16, const int32_t *row_o
  *   E_local); a token without such a slot gets 0. A token may name an expert
  *   twice (the weights add). Ids outside the range are not local.
  *   W = value(code) * scale as fq_dequantize_stacked defines it, without its
- *   rounding to bf16, except where the weight group is not a multiple of 64
- *   (int8, fp8), resp. 128 (int4), and not the whole row: then W is the bf16
- *   fake-quant value. Sums are fp32, in a fixed order (bitwise reproducible).
+ *   rounding to bf16 (within 2^-16 of it where the weight group is not a multiple
+ *   of 64 (int8, fp8), resp. 128 (int4), and not the whole row). Sums are fp32,
+ *   in a fixed order (bitwise reproducible).
  * fq_stored_w: fmt FQ_FMT_*, group as in fq_weight_q (int4: the whole row or a
  *   multiple of 32), codes [E, N, K] packed as exported (NONE: the raw bf16
  *   stack, group and the scales unused); scale (int8, fp8, int4),

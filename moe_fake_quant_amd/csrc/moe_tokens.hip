@@ -13,14 +13,16 @@
 // point, E2M1 times its E4M3 block scale: at most 8 significant bits) is a
 // bf16 number, and so is an activation's; the fp32 scales that are constant
 // over a contraction (per channel, per tensor, per 128-group, the NVFP4 tensor
-// scale, s_a) multiply the fp32 sums instead. Only weight groups that are no
-// multiple of a chunk (see Fmt) fold their scale into the operand, which rounds it to the
-// bf16 value the training forward uses. h stays in fp32. A without an activation
-// format is no grid value: it goes on as two bf16 numbers, A rounded and what that
-// leaves, each multiplied with the same weight operand. Together they are within
-// 2^-16 of A (half a bf16 step of half a bf16 step), so that the rounding of the
-// output is the only one that counts: against float64 the output is off by 0.0017
-// of its largest value, as with fp32 operands, where one bf16 A gives 0.0024.
+// scale, s_a) multiply the fp32 sums instead. h stays in fp32.
+//
+// Two operands are no grid values: A without an activation format, and weights in
+// groups that are no multiple of a chunk (see Fmt), whose scale enters the operand.
+// Each is taken as two bf16 numbers, the value rounded and what that leaves, with
+// an MFMA for either. Together they are within 2^-16 of it (half a bf16 step of half
+// a bf16 step), so that the rounding of the output is the only one that counts:
+// against float64 the output is off by 0.0017 (root mean squares), as with fp32
+// operands. One bf16 number for A gave 0.0024, one for the weights 0.0034 and, where
+// an activation quantizer follows, 0.0125 (FP8, groups of 32).
 //
 // Contraction: v_mfma_f32_16x16x32 (bf16, or f16: see operand) with 16 weight rows as the row operand
 // and up to 16 tokens as columns. A lane loads 16 bytes of codes of its row
@@ -190,16 +192,27 @@ struct Has {
   static constexpr bool kZp = FMT == FQ_FMT_INT4;
 };
 
-// The row operand of one MFMA, step st of a chunk: 8 consecutive elements of the
-// lane's row as grid values (bf16, or f16 with F16).
+// bf16 numbers to a weight
+template <int FMT, int MODE>
+constexpr int weight_parts() { return MODE == kPre && FMT != FQ_FMT_NVFP4 ? 2 : 1; }
+template <int N>
+struct Operand {
+  bf16x8_t p[N];
+};
+
+// The row operand of step st of a chunk: 8 consecutive elements of the lane's row
+// (bf16, or f16 with F16).
 //
 // VALU operations per 8 codes: E4M3 4 (the converter makes bf16 pairs), NVFP4
 // 8 in f16 (convert and multiply pairs by the block scale) or 16 through fp32
-// in bf16, int4 23, int8 about 16. f16 holds every NVFP4, E4M3 and int8 grid
+// in bf16, int4 23, int8 about 16, and 28 more for two parts. f16 holds every NVFP4, E4M3 and int8 grid
 // value exactly (at most 8 bits, 2^-10 <= |v| <= 2688), but not any bf16
 // activation, so it is used for quantized activations.
 template <int FMT, int MODE, bool F16>
-__device__ __forceinline__ bf16x8_t operand(const Codes &r, const Scales &q, int st) {
+__device__ __forceinline__ Operand<weight_parts<FMT, MODE>()> operand(const Codes &r,
+                                                                      const Scales &q, int st) {
+  constexpr int kParts = weight_parts<FMT, MODE>();
+  Operand<kParts> o;
   if (FMT == FQ_FMT_NVFP4 && F16) {
     const uint32_t c = r.w[st];
     const f16x2 th = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q.sb, 1.0f, false);
@@ -210,19 +223,19 @@ __device__ __forceinline__ bf16x8_t operand(const Codes &r, const Scales &q, int
     v[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 1) * ss;
     v[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 2) * ss;
     v[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.0f, 3) * ss;
-    return __builtin_bit_cast(bf16x8_t, v);
+    o.p[0] = __builtin_bit_cast(bf16x8_t, v);
+    return o;
   }
-  bf16x8_t o;
   if (FMT == FQ_FMT_NONE) {
-    o = {{r.w[0], r.w[1], r.w[2], r.w[3]}};
+    o.p[0] = {{r.w[0], r.w[1], r.w[2], r.w[3]}};
   } else if (FMT == FQ_FMT_FP8_E4M3 && MODE != kPre) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t c = r.w[2 * st + h];
-      o.w[2 * h] = __builtin_bit_cast(uint32_t,
-                                      __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false));
-      o.w[2 * h + 1] = __builtin_bit_cast(uint32_t,
-                                          __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true));
+      o.p[0].w[2 * h] = __builtin_bit_cast(
+          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false));
+      o.p[0].w[2 * h + 1] = __builtin_bit_cast(
+          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true));
     }
   } else {
     float v[8];
@@ -262,12 +275,20 @@ __device__ __forceinline__ bf16x8_t operand(const Codes &r, const Scales &q, int
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = v[j] * q.s0;
     }
-    o = pack8(v);
+    o.p[0] = pack8(v);
+    if constexpr (kParts == 2) {
+      float f[8];
+      unpack8(o.p[0], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] -= f[j];
+      o.p[1] = pack8(v);
+    }
   }
   return o;
 }
 
-// acc plus the products of a row operand and 8 activation values of its type
+// acc plus the products of a row operand and 8 activation values of its type.
+// Both in two parts: three products, the rests' own is below 2^-16 of the whole.
 template <bool F16>
 __device__ __forceinline__ f32x4 mfma(const bf16x8_t &o, const bf16x8_t &x, f32x4 acc) {
   if (F16)
@@ -275,6 +296,13 @@ __device__ __forceinline__ f32x4 mfma(const bf16x8_t &o, const bf16x8_t &x, f32x
                                                   __builtin_bit_cast(f16x8v, x), acc, 0, 0, 0);
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8v, o),
                                                  __builtin_bit_cast(bf16x8v, x), acc, 0, 0, 0);
+}
+template <bool F16, int WP, int XP>
+__device__ __forceinline__ f32x4 mfma(const Operand<WP> &o, const bf16x8_t (&x)[XP], f32x4 acc) {
+#pragma unroll
+  for (int h = 0; h < XP; ++h) acc = mfma<F16>(o.p[0], x[h], acc);
+  if constexpr (WP == 2) acc = mfma<F16>(o.p[1], x[0], acc);
+  return acc;
 }
 
 // the factor of a finished sum of one row of expert e
@@ -747,8 +775,8 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
           }
 #pragma unroll
           for (int st = 0; st < kSteps; ++st) {
-            const bf16x8_t b =
-                *reinterpret_cast<const bf16x8_t *>(xs + (ch * kChunk + st * 8) * 2);
+            const bf16x8_t b[1] = {
+                *reinterpret_cast<const bf16x8_t *>(xs + (ch * kChunk + st * 8) * 2)};
             s0 = mfma<F16>(operand<FMT, MODE, F16>(r[u][0], qg, st), b, s0);
             s1 = mfma<F16>(operand<FMT, MODE, F16>(r[u][1], qu, st), b, s1);
           }
@@ -855,7 +883,9 @@ template <int FMT, int MODE, bool F16, bool WHOLE, int PARTS>
 __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
   constexpr int kChunk = Fmt<FMT>::kChunk, kSeg = Fmt<FMT>::kSeg, kSteps = Fmt<FMT>::kSteps;
   constexpr bool kSb = Has<FMT, MODE>::kSb, kS = Has<FMT, MODE>::kS, kZp = Has<FMT, MODE>::kZp;
-  constexpr int kU = 4;                        // chunks whose codes are requested together
+  // chunks whose codes are requested together (4 of int4 in two parts would spill: 141 us
+  // where 2 take 138, 16 tokens in groups of 32)
+  constexpr int kU = FMT == FQ_FMT_INT4 && MODE == kPre ? 2 : 4;
   // chunks whose activations are: 32 registers of them
   constexpr int kB = FMT == FQ_FMT_NONE ? 4 : (Fmt<FMT>::k4bit ? 2 : 4) / PARTS;
   __shared__ int4 act[1024];
@@ -1000,11 +1030,8 @@ __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
       f32x4 s = {0, 0, 0, 0};
       if (MODE != kPost) s = acc;
 #pragma unroll
-      for (int st = 0; st < kSteps; ++st) {
-        const bf16x8_t o = operand<FMT, MODE, F16>(r.c[i], q, st);
-#pragma unroll
-        for (int h = 0; h < PARTS; ++h) s = mfma<F16>(o, b[i % kB][st][h], s);
-      }
+      for (int st = 0; st < kSteps; ++st)
+        s = mfma<F16>(operand<FMT, MODE, F16>(r.c[i], q, st), b[i % kB][st], s);
       if (MODE == kPost) {
         // weight row 4 kq + i of the result is lane 4 kq + i's row
 #pragma unroll

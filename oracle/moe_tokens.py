@@ -11,7 +11,9 @@ quantizer maps the moved interval onto grid values (an interval that crosses a
 rounding border takes the values of both sides). Without an activation format
 the other side may hold A as two bf16 numbers, A rounded (off by at most half a
 step, 2^-8 |A|) and the rest rounded (2^-8 of that): 2^-16 |A| in all, or half
-the smallest subnormal step, and a sum of twice as many products.
+the smallest subnormal step, and a sum of twice as many products. It may hold
+weights of small groups (stored_values' bf16 ones) alike, and leave out the
+product of the two rests, again 2^-16 of the whole: up to three products an element.
 """
 from __future__ import annotations
 
@@ -25,17 +27,27 @@ from .numerics import bf16_to_f32
 U = 2.0 ** -24
 
 
+class _Decoded(np.ndarray):
+    """A decoded stack whose values are bf16 numbers; exact: before the rounding."""
+
+    exact = None
+
+
+def _exact(w):
+    """A stack's values, and the bf16 parts that the other side may take them in."""
+    e = getattr(w, "exact", None)
+    return (np.asarray(w), 1) if e is None else (e, 2)
+
+
 def stored_values(w_bits, fmt: int, group: int, scale, zp=None, g=None):
     """float64 values of a stored stack [E, N, K]: value(code) * scale, or the
-    bf16 fake-quant value where the group is smaller than 64 (int8, fp8) or
-    not a multiple of 128 (int4) and not the whole row."""
+    bf16 fake-quant value (as fq_dequantize_stacked gives it) where the group is
+    smaller than 64 (int8, fp8) or not a multiple of 128 (int4) and not the whole
+    row. The layer multiplies with the values before that rounding."""
     fq = fq_weight_stack(w_bits, fmt, group, scale, zp, g)
     if fmt == FMT_NONE:
         return fq.v.astype(np.float64)
     E, N, K = fq.q.shape
-    if fmt in (FMT_INT8, FMT_FP8, FMT_INT4) and 0 < group < K \
-            and group % (128 if fmt == FMT_INT4 else 64):
-        return bf16_to_f32(fq.bits).astype(np.float64)
     if fmt == FMT_NVFP4:
         th = e4m3_round(np.clip(scale, 0, E4M3_MAX).astype(np.float32))[1]
         s = np.repeat(th, 16, axis=-1) * np.asarray(g, np.float64).reshape(E, 1, 1)
@@ -43,7 +55,12 @@ def stored_values(w_bits, fmt: int, group: int, scale, zp=None, g=None):
         s = np.asarray(scale, np.float64).reshape(E, 1, 1)
     else:
         s = np.repeat(np.asarray(scale, np.float64).reshape(E, N, K // group), group, axis=-1)
-    return fq.q * s
+    v = fq.q * s
+    if fmt in (FMT_INT8, FMT_FP8, FMT_INT4) and 0 < group < K \
+            and group % (128 if fmt == FMT_INT4 else 64):
+        v, exact = bf16_to_f32(fq.bits).astype(np.float64).view(_Decoded), v
+        v.exact = exact
+    return v
 
 
 def _quant(a, fmt, s, theta=None):
@@ -97,6 +114,7 @@ def moe_tokens(x_bits, ids, probs, ebegin: int, w_gu, w_d, afmt: int, s1, s2, re
     T = len(ids)
     E, F2, H = w_gu.shape
     F = F2 // 2
+    (w_gu, parts_gu), (w_d, parts_d) = _exact(w_gu), _exact(w_d)
     fx = fq_act(x_bits, afmt, s1)
     xq = fx.q * float(np.float32(s1)) if afmt in (FMT_FP8, FMT_INT8) else fx.v.astype(np.float64)
     out, tol = np.zeros((T, H)), np.zeros((T, H))
@@ -107,7 +125,8 @@ def moe_tokens(x_bits, ids, probs, ebegin: int, w_gu, w_d, afmt: int, s1, s2, re
             p = float(probs[t, j])
             h = w_gu[e] @ xq[t]
             # the scales outside the sum and the NVFP4 block scale's own rounding: 4 more
-            dh = (H + 36) * U * (np.abs(w_gu[e]) @ np.abs(xq[t])) + rel_h * np.abs(h)
+            dh = ((parts_gu * H + 36) * U + (parts_gu - 1) * 2.0 ** -16) \
+                * (np.abs(w_gu[e]) @ np.abs(xq[t])) + rel_h * np.abs(h)
             g, u = h[:F], h[F:]
             sg = _sigmoid(g)
             a = g * sg * u
@@ -118,7 +137,9 @@ def moe_tokens(x_bits, ids, probs, ebegin: int, w_gu, w_d, afmt: int, s1, s2, re
             A, dA = A[0], dA[0] + 4 * U * np.abs(A[0])
             o = w_d[e] @ A
             mag = np.abs(w_d[e]) @ np.abs(A)
-            n = 2 * F if afmt == FMT_NONE else F
+            parts_a = 2 if afmt == FMT_NONE else 1
+            two = (parts_d - 1) * parts_a * 2.0 ** -16
+            tol[t] += abs(p) * (np.abs(w_d[e]) @ dA + rel_h * np.abs(o)
+                                + (((parts_d + parts_a - 1) * F + 36) * U + two) * mag)
             out[t] += p * o
-            tol[t] += abs(p) * (np.abs(w_d[e]) @ dA + (n + 36) * U * mag + rel_h * np.abs(o))
     return out, tol + 80 * U * np.abs(out)

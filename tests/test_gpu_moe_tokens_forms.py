@@ -5,7 +5,7 @@ import pytest
 
 import oracle as O
 from test_gpu_moe_tokens import Call, make, run_case
-from test_oracle_moe_tokens_a import FORMS, difference_case
+from test_oracle_moe_tokens_a import FORMS, SMALL_GROUPS, difference_case
 from tokens_case import reference
 
 pytestmark = pytest.mark.gpu
@@ -19,6 +19,17 @@ def test_a_without_an_activation_format_is_not_rounded(fmt, group, T):
     call = Call(difference_case(100 + T, T, 3, 256, 256, fmt, group))
     call.run()
     call.check()
+
+
+@pytest.mark.parametrize("fmt,group", SMALL_GROUPS)
+@pytest.mark.parametrize("T", [1, 20])
+def test_weights_of_small_groups_are_not_rounded(fmt, group, T):
+    """Groups whose scales are no bf16 numbers, in rows that whole and ended chunks make."""
+    for H, Fc in ((256, 256), (288 if group == 32 else 208 if group == 16 else 320, 128)):
+        print(f"[tokens] weights fmt={fmt} group={group} T={T} H={H}", flush=True)
+        call = Call(difference_case(130 + T, T, 3, H, Fc, fmt, group, uneven=True))
+        call.run()
+        call.check()
 
 
 def test_a_beyond_the_largest_bf16_number():
