@@ -107,14 +107,17 @@ def quant_interval(lo, mid, hi, fmt, s):
     return v, d
 
 
-def moe_tokens(x_bits, ids, probs, ebegin: int, w_gu, w_d, afmt: int, s1, s2, rel_h: float = 0.0):
+def moe_tokens(x_bits, ids, probs, ebegin: int, w_gu, w_d, afmt: int, s1, s2, rel_h: float = 0.0,
+               afmt2=None):
     """out [T, H] float64 and its tolerance before the rounding to bf16.
     w_gu [E, 2F, H], w_d [E, H, F]: stored_values. rel_h: a further relative
-    error of h and of a that the other side may have."""
+    error of h and of a that the other side may have. afmt2: A's activation
+    format where it is not x's."""
     T = len(ids)
     E, F2, H = w_gu.shape
     F = F2 // 2
     (w_gu, parts_gu), (w_d, parts_d) = _exact(w_gu), _exact(w_d)
+    afmt2 = afmt if afmt2 is None else afmt2
     fx = fq_act(x_bits, afmt, s1)
     xq = fx.q * float(np.float32(s1)) if afmt in (FMT_FP8, FMT_INT8) else fx.v.astype(np.float64)
     out, tol = np.zeros((T, H)), np.zeros((T, H))
@@ -133,11 +136,11 @@ def moe_tokens(x_bits, ids, probs, ebegin: int, w_gu, w_d, afmt: int, s1, s2, re
             # |silu'| <= 1.1; sigmoid's own error as |g| 2^-23 and a few ulp
             da = (1.1 * dh[:F] * (np.abs(u) + dh[F:]) + np.abs(g * sg) * dh[F:]
                   + np.abs(a) * ((np.abs(g) + 10) * 2 * U + rel_h))
-            A, dA = quant_interval((a - da)[None], a[None], (a + da)[None], afmt, s2)
+            A, dA = quant_interval((a - da)[None], a[None], (a + da)[None], afmt2, s2)
             A, dA = A[0], dA[0] + 4 * U * np.abs(A[0])
             o = w_d[e] @ A
             mag = np.abs(w_d[e]) @ np.abs(A)
-            parts_a = 2 if afmt == FMT_NONE else 1
+            parts_a = 2 if afmt2 == FMT_NONE else 1
             two = (parts_d - 1) * parts_a * 2.0 ** -16
             tol[t] += abs(p) * (np.abs(w_d[e]) @ dA + rel_h * np.abs(o)
                                 + (((parts_d + parts_a - 1) * F + 36) * U + two) * mag)

@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 
 import oracle as O
-from test_gpu_moe_tokens import Call, make, run_case
+from helpers import dev_f32
+from test_gpu_moe_tokens import Call, F, make, run_case
 from test_oracle_moe_tokens_a import FORMS, SMALL_GROUPS, difference_case
 from tokens_case import reference
 
@@ -131,3 +132,26 @@ def test_items_of_several_channel_groups(fmt, group, afmt, H, mt):
 def test_wide_rows_of_small_groups_two_channel_groups(fmt, afmt):
     """Rows that end inside a chunk, 64 of them with their scales in LDS."""
     run_case(seed=111, T=9, E=3, H=4112, F=48, topk=2, fmt=fmt, group=16, afmt=afmt)
+
+
+ACTS = {O.FMT_NONE: 1.0, O.FMT_FP8: 448.0, O.FMT_INT8: 127.0, O.FMT_NVFP4: 2688.0}
+CROSSED = [(O.FMT_NVFP4, 16, O.FMT_NVFP4, O.FMT_NONE), (O.FMT_NVFP4, 16, O.FMT_NONE, O.FMT_NVFP4),
+           (O.FMT_NVFP4, 16, O.FMT_FP8, O.FMT_INT8), (O.FMT_NVFP4, 16, O.FMT_INT8, O.FMT_FP8),
+           (O.FMT_INT8, None, O.FMT_NVFP4, O.FMT_NVFP4), (O.FMT_INT8, 32, O.FMT_FP8, O.FMT_NONE),
+           (O.FMT_FP8, 64, O.FMT_NONE, O.FMT_INT8), (O.FMT_FP8, O.GROUP_TENSOR, O.FMT_INT8, O.FMT_NVFP4),
+           (O.FMT_INT4, 64, O.FMT_NVFP4, O.FMT_INT8), (O.FMT_INT4, 128, O.FMT_INT8, O.FMT_NVFP4),
+           (O.FMT_NONE, 0, O.FMT_FP8, O.FMT_NVFP4), (O.FMT_NONE, 0, O.FMT_NVFP4, O.FMT_FP8)]
+
+
+@pytest.mark.parametrize("fmt,group,a1,a2", CROSSED)
+def test_activation_formats_of_their_own(fmt, group, a1, a2):
+    """Weights under another format's activations, x and A in different ones."""
+    print(f"[tokens] fmt={fmt} group={group} a1={a1} a2={a2}", flush=True)
+    c = make(seed=140, T=11, E=6, H=256, F=128, topk=3, fmt=fmt, group=group, afmt=O.FMT_NONE)
+    c["s1"] = np.float32(c["s1"] / ACTS[a1])
+    c["s2"] = np.float32(c["s2"] / ACTS[a2])
+    call = Call(c)
+    call.a1, call.a2 = F.ActQ(a1, dev_f32([c["s1"]])), F.ActQ(a2, dev_f32([c["s2"]]))
+    call.run()
+    vals = [O.stored_values(bits, f, g, *q) for f, g, bits, q in (c["gu"], c["d"])]
+    call.check(O.moe_tokens(c["x"], c["ids"], c["probs"], 0, *vals, a1, c["s1"], c["s2"], afmt2=a2))
