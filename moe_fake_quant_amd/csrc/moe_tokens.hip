@@ -5,9 +5,11 @@
 //   k_tok_gate_up  h = W_gu[e] FQ_a1(x),  a = silu(h_g) h_u,  A = FQ_a2(a)
 //   k_tok_down     out[t] = bf16(sum_j p[t,j] W_d[e_tj] A[t,j])
 //
-// What bounds it: the codes of the distinct experts of the batch are read once
-// and everything else is small, so the floor is the weight stream from HBM;
-// next come the VALU operations that turn 4-bit codes into MFMA operands.
+// What bounds it: the codes of the distinct experts of the batch are read and
+// everything else is small, so the floor is the weight stream from HBM; next
+// come the VALU operations that turn 4-bit codes into MFMA operands. An expert
+// of more rows than one pass of columns takes (16 or what fits into LDS in
+// gate_up, 8 in down) has its codes loaded and decoded again for each pass.
 //
 // Operands are exact. A weight's grid value (E4M3, int8, int4 minus zero
 // point, E2M1 times its E4M3 block scale: at most 8 significant bits) is a
@@ -31,9 +33,9 @@
 // 16 rows x 64 contiguous bytes.
 //
 // Measured at 128 experts, H 2048, F 768, top 8 (gate_up + down, us; the bytes of
-// the named experts): NVFP4, 1 token 13.5 + 5.5 (21 MB, latency); 64 tokens 62 + 40
-// (226 + 109 MB: 3.7 and 2.7 TB/s); FP8, 16 tokens 52 + 31 (260 + 130 MB: 5.0 and
-// 4.2 TB/s); INT4 with bf16 activations, 7 tokens 38 + 20. A 1 GiB device copy runs
+// the named experts): NVFP4, 1 token 13.5 + 5.4 (21 MB, latency); 64 tokens 61 + 41
+// (226 + 109 MB: 3.7 and 2.7 TB/s); FP8, 16 tokens 53 + 31 (260 + 130 MB: 4.9 and
+// 4.2 TB/s); INT4 with bf16 activations, 7 tokens 39 + 24. A 1 GiB device copy runs
 // at 5.2 TB/s.
 //
 // Sums are taken in a fixed order (no float atomics): the same call gives the
@@ -555,8 +557,8 @@ __device__ __forceinline__ size_t a_offset(int seg, int parts, int f, int row, i
 // eight waves are MT channel groups (gate and up rows of the same 16 channels)
 // times 8 / MT shares of the contraction. The first weights of an item are
 // requested before the sums of the one before are added up. (One block per item
-// with a plan and staging of its own took 98 us where this takes 62: 64 tokens,
-// NVFP4; its streaming phase then runs at 6 TB/s behind a start of 12 us.)
+// with a plan and staging of its own took 98 us where this takes 61: 64 tokens,
+// NVFP4, 227 MB. A launch for one token, all latency, takes 13.5 us.)
 template <int FMT, int MODE, bool F16, bool WHOLE, int MT>
 __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
   constexpr int kChunk = Fmt<FMT>::kChunk, kSeg = Fmt<FMT>::kSeg, kSteps = Fmt<FMT>::kSteps;
@@ -878,7 +880,8 @@ __global__ __launch_bounds__(kNT, 4) void k_tok_gate_up(TokArgs a) {
 // waves' blocks are added in wave order. (Splitting the experts over blocks, the
 // last one adding the parts, cost 40 us in device-wide fences alone.) Bound by its
 // gather loads: 64 tokens took 47 us with A row by row, 34 without the A loads, 33
-// without the weight loads, and 40 with A in its present order.
+// without the weight loads, and 40 with A in its present order. H / 8 blocks are one
+// round of the CUs at H = 2048; narrower layers leave CUs idle.
 template <int FMT, int MODE, bool F16, bool WHOLE, int PARTS>
 __global__ __launch_bounds__(kNTd) void k_tok_down(TokArgs a) {
   constexpr int kChunk = Fmt<FMT>::kChunk, kSeg = Fmt<FMT>::kSeg, kSteps = Fmt<FMT>::kSteps;

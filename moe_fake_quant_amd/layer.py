@@ -28,7 +28,7 @@ With ``ckpt`` the forward keeps h (and the layer input) for the backward as
 8-bit checkpoints instead of bf16: the SwiGLU pass saves h, the backward decodes
 it in registers and re-forms FQ_a(A) for the down projection's dScale. What a
 layer then holds from its forward to its backward is the codes with their
-scales, 2F + H/topk bytes a routed row (and 3 to 25 % for the scales) instead of
+scales, 2F + H/topk bytes a routed row (and 0.8 to 25 % for the scales) instead of
 6F + 2H/topk; every other buffer is free in between, and ``scratch_of`` lets the
 layers of a model share one set of them.
 
