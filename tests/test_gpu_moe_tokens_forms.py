@@ -2,9 +2,10 @@
 not launch, by the same bound."""
 import numpy as np
 import pytest
+import torch
 
 import oracle as O
-from helpers import dev_f32
+from helpers import dev_bf16, dev_f32, dev_i32
 from test_gpu_moe_tokens import Call, F, make, run_case
 from test_oracle_moe_tokens_a import FORMS, SMALL_GROUPS, difference_case
 from tokens_case import reference
@@ -155,3 +156,41 @@ def test_activation_formats_of_their_own(fmt, group, a1, a2):
     call.run()
     vals = [O.stored_values(bits, f, g, *q) for f, g, bits, q in (c["gu"], c["d"])]
     call.check(O.moe_tokens(c["x"], c["ids"], c["probs"], 0, *vals, a1, c["s1"], c["s2"], afmt2=a2))
+
+
+@pytest.mark.parametrize("fmt,group,afmt", [(O.FMT_NVFP4, 16, O.FMT_NVFP4),
+                                            (O.FMT_INT4, 32, O.FMT_NONE)])
+def test_replays_with_new_tokens(fmt, group, afmt):
+    """One captured call, its tokens, routing and weights overwritten between the
+    replays (other experts, a hot one, none local at all), eager calls of another
+    size over the same workspace in between."""
+    c = make(seed=150, T=23, E=24, H=256, F=128, topk=4, fmt=fmt, group=group, afmt=afmt)
+    call, eager = Call(c), Call(c)
+    small = Call(dict(c, T=2, x=c["x"][:2], ids=c["ids"][:2], probs=c["probs"][:2]))
+    small.ws = call.ws
+    call.run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call.run()
+    rng = np.random.default_rng(151)
+    for step in range(5):
+        ids = np.stack([rng.permutation(24)[:4] for _ in range(23)]).astype(np.int32)
+        if step == 1:
+            ids[:, 2] = 5
+        if step == 3:
+            ids[:] = 24
+        new = (dev_bf16(O.f32_to_bf16(rng.standard_normal((23, 256)).astype(np.float32))),
+               dev_i32(ids), dev_f32(rng.uniform(0.1, 1.0, (23, 4)).astype(np.float32)))
+        for k in (call, eager):
+            for to, v in zip((k.x, k.ids, k.p), new):
+                to.copy_(v)
+        call.out.fill_(7.0)
+        g.replay()
+        eager.run()
+        torch.cuda.synchronize()
+        assert torch.equal(call.out.view(torch.int16), eager.out.view(torch.int16)), step
+        assert bool(eager.out[:23].any()) == (step != 3)
+        small.run()
+        call.ws.fill_(0xFF)
+        torch.cuda.synchronize()
