@@ -26,8 +26,8 @@
 // operands. One bf16 number for A gave 0.0024, one for the weights 0.0034 and, where
 // an activation quantizer follows, 0.0125 (FP8, groups of 32).
 //
-// Contraction: v_mfma_f32_16x16x32 (bf16, or f16: see operand) with 16 weight rows as the row operand
-// and up to 16 tokens as columns. A lane loads 16 bytes of codes of its row
+// Contraction: v_mfma_f32_16x16x32 (bf16, or f16: see operand) with 16 weight rows
+// as the row operand and up to 16 tokens as columns. A lane loads 16 bytes of codes of its row
 // at once (32 four-bit codes) and feeds them to consecutive MFMAs, so the
 // contraction order is permuted, alike for both operands: a wave's load covers
 // 16 rows x 64 contiguous bytes.
@@ -207,9 +207,9 @@ struct Operand {
 //
 // VALU operations per 8 codes: E4M3 4 (the converter makes bf16 pairs), NVFP4
 // 8 in f16 (convert and multiply pairs by the block scale) or 16 through fp32
-// in bf16, int4 23, int8 about 16, and 28 more for two parts. f16 holds every NVFP4, E4M3 and int8 grid
-// value exactly (at most 8 bits, 2^-10 <= |v| <= 2688), but not any bf16
-// activation, so it is used for quantized activations.
+// in bf16, int4 23, int8 about 16, and 20 more for two parts. f16 holds every
+// NVFP4, E4M3 and int8 grid value exactly (at most 8 bits, 2^-10 <= |v| <= 2688),
+// but not any bf16 activation, so it is used for quantized activations.
 template <int FMT, int MODE, bool F16>
 __device__ __forceinline__ Operand<weight_parts<FMT, MODE>()> operand(const Codes &r,
                                                                       const Scales &q, int st) {
