@@ -29,8 +29,9 @@ With ``ckpt`` the forward keeps h (and the layer input) for the backward as
 it in registers and re-forms FQ_a(A) for the down projection's dScale. What a
 layer then holds from its forward to its backward is the codes with their
 scales, 2F + H/topk bytes a routed row (and 0.8 to 25 % for the scales) instead of
-6F + 2H/topk; every other buffer is free in between, and ``scratch_of`` lets the
-layers of a model share one set of them.
+6F + 2H/topk, beside its weights, scales and routing; every other activation
+buffer is free in between, and ``scratch_of`` lets the layers of a model share
+one set of them.
 
 After training, ``export()`` gives the stored form of both stacks and
 ``forward_tokens`` runs up to 128 tokens on it, as a decoding loop does.
