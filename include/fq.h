@@ -563,6 +563,105 @@ fq_status fq_swiglu_bwd_ckpt(const uint16_t *daq_bf16, const uint8_t *codes, con
                              uint16_t *aq_bf16, float *dscale_a, void *ws, size_t ws_bytes,
                              fq_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Products over int8 codes: the w8a8 preset (mcore_qad article, section 三) run
+ * on its stored codes instead of decoded bf16 weights, for any number of rows,
+ * with activations quantized as they come (one scale a token).
+ *
+ * fq_quantize_tokens: the int8 codes of token rows. x [rows, K] bf16 ->
+ *   codes [rows, K] (two's complement), scale [rows]: s = max(amax *
+ *   fp32(1/127), 2^-126), 1 for a row of zeros; r = 1/s, code = rne(clamp(x * r)).
+ *   A row with an infinity or NaN stores s = NaN and codes 0, so that its
+ *   outputs are NaN. n_rows as for the checkpoints (device, NULL = all rows).
+ * fq_grouped_gemm_int8: y[r, n] = bf16((sum_k cx[r, k] cw[e, n, k]) * sx[r] *
+ *   sw[e, n]) for the rows r of segment e = [seg_offsets[e], seg_offsets[e+1]);
+ *   the sum is exact (int32), the scales multiply in fp32.
+ * fq_grouped_gated_int8: shape {E, 2F, H}: g and u such sums over rows f and
+ *   F + f of the stack, a[r, f] = bf16(silu(g) * u) [R_max, F].
+ *   x_codes [x_rows, K], x_scale [x_rows]. perm NULL: routed row r is row r of x
+ *   (x_rows >= R_max); else row perm[r] / topk of x (perm as fq_moe_permute
+ *   gives it, x_rows = T). w: FQ_FMT_INT8 codes [E, N, K] as exported, group = K
+ *   (scale [E, N]) or FQ_GROUP_TENSOR (scale [E]); the other fields unused.
+ *   Rows from seg_offsets[E] on are left untouched.
+ * K and N (gated: F) multiples of 16, K <= 131071, E <= 1024; an expert's codes,
+ * and with perm the token rows, below 4 GiB. codes, x_codes, y and a 16-byte
+ * aligned, scales 4-byte. Workspace: fq_workspace_bytes(FQ_OP_GEMM_INT8, shape,
+ * R_max, 0), for the gated product FQ_OP_GATED.
+ * ---------------------------------------------------------------------- */
+fq_status fq_quantize_tokens(const uint16_t *x_bf16, int32_t rows, int32_t K, const int32_t *n_rows,
+                             uint8_t *codes, float *scale, fq_stream stream);
+fq_status fq_grouped_gemm_int8(const uint8_t *x_codes, const float *x_scale, int32_t x_rows,
+                               const int32_t *perm, int32_t topk, int32_t R_max,
+                               const int32_t *seg_offsets, fq_shape shape, const fq_stored_w *w,
+                               uint16_t *y_bf16, void *ws, size_t ws_bytes, fq_stream stream);
+fq_status fq_grouped_gated_int8(const uint8_t *x_codes, const float *x_scale, int32_t x_rows,
+                                const int32_t *perm, int32_t topk, int32_t R_max,
+                                const int32_t *seg_offsets, fq_shape shape, const fq_stored_w *w,
+                                uint16_t *a_bf16, void *ws, size_t ws_bytes, fq_stream stream);
+
+/* ------------------------------------------------------------------------
+ * The gated feed-forward block in one kernel: both projections of the fused
+ * gate_up stack (gate = first F rows), SwiGLU and the activation fake-quant
+ * (mcore_qad article, sections 二.3 and 二.4). h [R, 2F] is never written, and
+ * the backward forms it again from x (section 四: activation recompute).
+ *   g = x[row] . w_fq[e, f], u = x[row] . w_fq[e, F + f]     fp32, not rounded
+ *   a = bf16(silu(g) * u)
+ * fq_grouped_gated_fwd: aq = FQ_a(a) [R_max, F] (aq NULL or NONE: a itself).
+ * fq_grouped_gated_bwd: with s = sigmoid(g), m_a the activation-FQ mask of a:
+ *   da = m_a * daq, dh = [da*u*s*(1+g*(1-s)), da*g*s] [R_max, 2F] bf16;
+ *   aq_bf16 (or NULL) receives FQ_a(a). dx and dScale follow from dh by
+ *   fq_grouped_gemm_bwd_scale / fq_grouped_gemm_wgrad_tokens. daq [R_max, F].
+ * shape {E, 2F, H}; w_fq [E, 2F, H] bf16, used as given (fq_quantize_stacked's
+ * output, or the raw weights). x_bf16 [x_rows, H] already fake-quantized, read
+ * through perm / topk or (perm NULL) by routed row, as for the int8 products.
+ * Rows from seg_offsets[E] on are left untouched. H, F % 16 == 0, E <= 1024; an
+ * expert's matrix, and with perm the token rows, below 4 GiB.
+ * Workspace: fq_workspace_bytes(FQ_OP_GATED, shape, R_max, 0).
+ * ---------------------------------------------------------------------- */
+fq_status fq_grouped_gated_fwd(const uint16_t *x_bf16, int32_t x_rows, const int32_t *perm,
+                               int32_t topk, int32_t R_max, const int32_t *seg_offsets,
+                               fq_shape shape, const uint16_t *w_fq, const fq_act_q *aq,
+                               uint16_t *aq_bf16, void *ws, size_t ws_bytes, fq_stream stream);
+fq_status fq_grouped_gated_bwd(const uint16_t *daq_bf16, const uint16_t *x_bf16, int32_t x_rows,
+                               const int32_t *perm, int32_t topk, int32_t R_max,
+                               const int32_t *seg_offsets, fq_shape shape, const uint16_t *w_fq,
+                               const fq_act_q *aq, uint16_t *dh_bf16, uint16_t *aq_bf16, void *ws,
+                               size_t ws_bytes, fq_stream stream);
+
+/* ------------------------------------------------------------------------
+ * The norms before and after a block, with its gate and residual scale: what
+ * joins a layer to the residual stream (the layer's input norm, and around the
+ * MoE output a norm, a token's gate and a scale).
+ *   p = b * rsqrt(mean(b^2) + eps) * w_post     (w_post NULL: p = b)
+ *   y = x + alpha * gate[t] * p                 (gate NULL: 1; b NULL: y = x)
+ *   n = y * rsqrt(mean(y^2) + eps) * w_pre      the next layer's input
+ * fq_norm_residual_fwd: x, b [T, H] bf16; gate [T] fp32; w_post, w_pre [H] bf16.
+ *   Outputs, each may be NULL: y [T, H] bf16 (may be x itself); n [T, H] bf16;
+ *   codes [T, H] with scale [T] (n as fq_quantize_tokens defines them, from the
+ *   fp32 n). n comes from the unrounded y. w_pre if and only if n or codes.
+ * fq_norm_residual_bwd: from dy, dn (gradients of y and n; one may be NULL), the
+ *   stored y (needed with dn) and b. Each output may be NULL:
+ *   gy = dy + the norm's backward of dn (at the stored y, fp32)
+ *   dx = bf16(gy); dgate[t] = alpha * sum_h gy p; dp = alpha * gate[t] * gy;
+ *   db = the norm's backward of dp (w_post NULL: dp), bf16;
+ *   dw_post[h] = sum_t dp b rsqrt(mean(b^2) + eps), dw_pre[h] = sum_t dn y
+ *   rsqrt(mean(y^2) + eps), fp32, overwritten, summed in a fixed order.
+ *   dx may be dy or dn itself, db may be b itself; outputs must not overlap
+ *   otherwise. Workspace, with dw_post or dw_pre: fq_workspace_bytes(FQ_OP_NORM,
+ *   {1, T, H}, 0, 0).
+ * H % 16 == 0, H <= 16384; bf16 tensors and codes 16-byte aligned; eps > 0.
+ * ---------------------------------------------------------------------- */
+fq_status fq_norm_residual_fwd(const uint16_t *x_bf16, const uint16_t *b_bf16, const float *gate,
+                               float alpha, const uint16_t *w_post_bf16, const uint16_t *w_pre_bf16,
+                               float eps, int32_t T, int32_t H, uint16_t *y_bf16, uint16_t *n_bf16,
+                               uint8_t *codes, float *scale, fq_stream stream);
+fq_status fq_norm_residual_bwd(const uint16_t *dy_bf16, const uint16_t *dn_bf16,
+                               const uint16_t *y_bf16, const uint16_t *b_bf16, const float *gate,
+                               float alpha, const uint16_t *w_post_bf16, const uint16_t *w_pre_bf16,
+                               float eps, int32_t T, int32_t H, uint16_t *dx_bf16, uint16_t *db_bf16,
+                               float *dgate, float *dw_post, float *dw_pre, void *ws, size_t ws_bytes,
+                               fq_stream stream);
+
 /* Workspace sizing. op: one of FQ_OP_*. fmts = weight fmt | act fmt << 8. */
 #define FQ_OP_PERMUTE 1
 #define FQ_OP_GEMM_FWD 2
@@ -570,6 +669,9 @@ fq_status fq_swiglu_bwd_ckpt(const uint16_t *daq_bf16, const uint8_t *codes, con
 #define FQ_OP_ACT_SCALE_GRAD 4 /* shape = {1, rows, cols}; R_max, fmts unused */
 #define FQ_OP_TOPK_KL 5        /* shape, R_max, fmts unused */
 #define FQ_OP_MOE_TOKENS 6     /* shape = {E_local, H, F}, R_max = T * topk, fmts = topk */
+#define FQ_OP_GEMM_INT8 7      /* fmts unused */
+#define FQ_OP_GATED 8          /* shape = {E, 2F, H}; fmts unused */
+#define FQ_OP_NORM 9           /* shape = {1, T, H}; R_max, fmts unused */
 size_t fq_workspace_bytes(int32_t op, fq_shape shape, int32_t R_max, int32_t fmts);
 
 const char *fq_last_error(void);

@@ -40,6 +40,9 @@ FQ_OP_GEMM_BWD = 3
 FQ_OP_ACT_SCALE_GRAD = 4
 FQ_OP_TOPK_KL = 5
 FQ_OP_MOE_TOKENS = 6
+FQ_OP_GEMM_INT8 = 7
+FQ_OP_GATED = 8
+FQ_OP_NORM = 9
 FQ_GROUP_TENSOR = -1     # one weight scale per expert matrix (int8 / fp8)
 
 EXPORTED = (
@@ -49,7 +52,9 @@ EXPORTED = (
     "fq_last_error", "fq_abi_version", "fq_export_scales", "fq_dequantize_stacked", "fq_topk_kl",
     "fq_moe_permute_noalloc", "fq_validate", "fq_actfq", "fq_grouped_gemm_fwd_tokens",
     "fq_grouped_gemm_wgrad_tokens", "fq_ckpt_save", "fq_ckpt_load", "fq_swiglu_actfq_ckpt",
-    "fq_swiglu_bwd_ckpt", "fq_moe_tokens",
+    "fq_swiglu_bwd_ckpt", "fq_moe_tokens", "fq_quantize_tokens", "fq_grouped_gemm_int8",
+    "fq_grouped_gated_int8", "fq_grouped_gated_fwd", "fq_grouped_gated_bwd", "fq_norm_residual_fwd",
+    "fq_norm_residual_bwd",
 )
 
 FQ_BAD_EXPERT_ID = 0x01
@@ -93,6 +98,7 @@ def _load() -> ctypes.CDLL:
                           "`python moe_fake_quant_amd/build.py` (hipcc, gfx950)")
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    F32 = ctypes.c_float
     st = ctypes.c_int
     sig = {
         "observer_absmax_init": (st, [P, fq_shape, I32, I32, I32, P, P, P, P, SZ, P]),
@@ -130,6 +136,18 @@ def _load() -> ctypes.CDLL:
                                       P, P]),
         "fq_swiglu_bwd_ckpt": (st, [P, P, P, I32, P, I32, I32, I32, ctypes.POINTER(fq_act_q), P, P,
                                     P, P, SZ, P]),
+        "fq_quantize_tokens": (st, [P, I32, I32, P, P, P, P]),
+        "fq_grouped_gemm_int8": (st, [P, P, I32, P, I32, I32, P, fq_shape,
+                                      ctypes.POINTER(fq_stored_w), P, P, SZ, P]),
+        "fq_grouped_gated_int8": (st, [P, P, I32, P, I32, I32, P, fq_shape,
+                                       ctypes.POINTER(fq_stored_w), P, P, SZ, P]),
+        "fq_grouped_gated_fwd": (st, [P, I32, P, I32, I32, P, fq_shape, P, ctypes.POINTER(fq_act_q), P,
+                                      P, SZ, P]),
+        "fq_grouped_gated_bwd": (st, [P, P, I32, P, I32, I32, P, fq_shape, P, ctypes.POINTER(fq_act_q),
+                                      P, P, P, SZ, P]),
+        "fq_norm_residual_fwd": (st, [P, P, P, F32, P, P, F32, I32, I32, P, P, P, P, P]),
+        "fq_norm_residual_bwd": (st, [P, P, P, P, P, F32, P, P, F32, I32, I32, P, P, P, P, P, P, SZ,
+                                      P]),
         "fq_workspace_bytes": (SZ, [I32, fq_shape, I32, I32]),
         "fq_last_error": (ctypes.c_char_p, []),
         "fq_abi_version": (I32, []),
@@ -178,12 +196,13 @@ def _stream():
     return _raw_stream(torch.cuda.current_device())
 
 
-def _same_device(t: Optional[torch.Tensor]):
+def _same_device(*tensors: Optional[torch.Tensor]):
     """The calls run on the current device's stream; its kernels must not be
     handed another device's memory."""
-    if t is not None and t.is_cuda and t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
 
 
 @dataclasses.dataclass
@@ -401,6 +420,60 @@ def fq_topk_kl(student, teacher, T, V, K, reverse, valid, topk_idx, grad, loss_t
     _check(_lib.fq_topk_kl(_p(student), _p(teacher), int(T), int(V), int(K), int(bool(reverse)),
                            _p(valid), _p(topk_idx), _p(grad), _p(loss_tok), _p(loss_mean), _p(ws),
                            _nbytes(ws), _stream()))
+
+
+def fq_quantize_tokens(x, rows, K, n_rows, codes, scale):
+    _same_device(x, codes, scale)
+    _check(_lib.fq_quantize_tokens(_p(x), int(rows), int(K), _p(n_rows), _p(codes), _p(scale),
+                                   _stream()))
+
+
+def fq_grouped_gemm_int8(x_codes, x_scale, x_rows, perm, topk, R_max, seg_offsets, shape, w: StoredW,
+                         y, ws=None):
+    _same_device(x_codes, w.codes, y, ws)
+    _check(_lib.fq_grouped_gemm_int8(_p(x_codes), _p(x_scale), int(x_rows), _p(perm), int(topk),
+                                     int(R_max), _p(seg_offsets), _shape(*shape),
+                                     ctypes.byref(w.c()), _p(y), _p(ws), _nbytes(ws), _stream()))
+
+
+def fq_grouped_gated_int8(x_codes, x_scale, x_rows, perm, topk, R_max, seg_offsets, shape, w: StoredW,
+                          a, ws=None):
+    _same_device(x_codes, w.codes, a, ws)
+    _check(_lib.fq_grouped_gated_int8(_p(x_codes), _p(x_scale), int(x_rows), _p(perm), int(topk),
+                                      int(R_max), _p(seg_offsets), _shape(*shape),
+                                      ctypes.byref(w.c()), _p(a), _p(ws), _nbytes(ws), _stream()))
+
+
+def fq_grouped_gated_fwd(x, x_rows, perm, topk, R_max, seg_offsets, shape, w_fq, aq: Optional[ActQ],
+                         aq_out, ws=None):
+    _same_device(x, w_fq, aq_out, ws)
+    _check(_lib.fq_grouped_gated_fwd(_p(x), int(x_rows), _p(perm), int(topk), int(R_max),
+                                     _p(seg_offsets), _shape(*shape), _p(w_fq), _aq(aq), _p(aq_out),
+                                     _p(ws), _nbytes(ws), _stream()))
+
+
+def fq_grouped_gated_bwd(daq, x, x_rows, perm, topk, R_max, seg_offsets, shape, w_fq,
+                         aq: Optional[ActQ], dh, aq_out=None, ws=None):
+    _same_device(daq, x, w_fq, dh, ws)
+    _check(_lib.fq_grouped_gated_bwd(_p(daq), _p(x), int(x_rows), _p(perm), int(topk), int(R_max),
+                                     _p(seg_offsets), _shape(*shape), _p(w_fq), _aq(aq), _p(dh),
+                                     _p(aq_out), _p(ws), _nbytes(ws), _stream()))
+
+
+def fq_norm_residual_fwd(x, b, gate, alpha, w_post, w_pre, eps, T, H, y=None, n=None, codes=None,
+                         scale=None):
+    _same_device(x, b, y, n, codes)
+    _check(_lib.fq_norm_residual_fwd(_p(x), _p(b), _p(gate), float(alpha), _p(w_post), _p(w_pre),
+                                     float(eps), int(T), int(H), _p(y), _p(n), _p(codes), _p(scale),
+                                     _stream()))
+
+
+def fq_norm_residual_bwd(dy, dn, y, b, gate, alpha, w_post, w_pre, eps, T, H, dx=None, db=None,
+                         dgate=None, dw_post=None, dw_pre=None, ws=None):
+    _same_device(dy, dn, y, b, dx, db, ws)
+    _check(_lib.fq_norm_residual_bwd(_p(dy), _p(dn), _p(y), _p(b), _p(gate), float(alpha), _p(w_post),
+                                     _p(w_pre), float(eps), int(T), int(H), _p(dx), _p(db), _p(dgate),
+                                     _p(dw_post), _p(dw_pre), _p(ws), _nbytes(ws), _stream()))
 
 
 from .layer import MoEFakeQuantLayer  # noqa: E402,F401

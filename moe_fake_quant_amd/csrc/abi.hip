@@ -226,6 +226,69 @@ fq_status check_ckpt(int64_t rows, int64_t K, int gdim, int fmt, int group, cons
   return FQ_OK;
 }
 
+// Sizes, row map and alignment that the int8 and gated products share; elem:
+// bytes of an operand's element, outputs: N or, gated, N / 2 columns.
+fq_status check_product(const void *x, int64_t x_rows, const int32_t *perm, int32_t topk,
+                        int32_t R_max, const int32_t *seg, fq_shape s, bool gated, int elem,
+                        const void *out) {
+  FQ_TRY(check_shape(s));
+  FQ_CHECK_ARG(R_max >= 0 && x_rows >= 0, "R_max < 0 or x_rows < 0");
+  FQ_CHECK_ARG(seg != nullptr, "seg_offsets is NULL");
+  FQ_CHECK_ARG(R_max == 0 || (x && out), "NULL pointer");
+  FQ_CHECK_ARG(!perm || topk > 0, "perm needs topk > 0 (topk=%d)", topk);
+  FQ_CHECK_ARG(perm || x_rows >= R_max, "x has %lld rows, R_max is %d", (long long)x_rows, R_max);
+  FQ_CHECK_SUPPORTED(s.N % (gated ? 32 : 16) == 0 && s.K % 16 == 0,
+                     gated ? "the gated block needs F %% 16 == 0 and H %% 16 == 0 (2F=%d H=%d)"
+                           : "the int8 product needs N %% 16 == 0 and K %% 16 == 0 (N=%d K=%d)",
+                     s.N, s.K);
+  FQ_CHECK_SUPPORTED(s.E <= 1024, "up to 1024 experts per stack (E=%d)", s.E);
+  FQ_CHECK_SUPPORTED((size_t)s.N * s.K * elem < (1ull << 32) &&
+                         (!perm || (size_t)x_rows * s.K * elem < (1ull << 32)),
+                     "an expert's matrix and the token rows must stay below 4 GiB (32-bit offsets)");
+  FQ_CHECK_ARG((!x || aligned16(x)) && (!out || aligned16(out)), "tensors must be 16-byte aligned");
+  return FQ_OK;
+}
+
+// int8 codes [E, N, K] with a scale for each output channel or each matrix
+fq_status check_int8_w(const fq_stored_w *w, fq_shape s) {
+  FQ_CHECK_ARG(w != nullptr, "w is NULL");
+  FQ_CHECK_SUPPORTED(w->fmt == FQ_FMT_INT8, "the int8 product takes int8 codes (fmt %d)", w->fmt);
+  FQ_CHECK_SUPPORTED(w->group == s.K || w->group == FQ_GROUP_TENSOR,
+                     "the int8 product takes one scale a channel (group = K) or a matrix "
+                     "(FQ_GROUP_TENSOR), not groups of %d", w->group);
+  FQ_CHECK_SUPPORTED(s.K <= kInt8MaxK, "K=%d: the int32 sums hold K <= %d", s.K, kInt8MaxK);
+  FQ_CHECK_ARG(w->codes && aligned16(w->codes), "codes must be non-NULL, 16-byte aligned");
+  FQ_CHECK_ARG(w->scale && (reinterpret_cast<uintptr_t>(w->scale) & 3u) == 0,
+               "scale must be non-NULL, 4-byte aligned");
+  return FQ_OK;
+}
+
+fq_status int8_call(const char *fn, bool gated, const uint8_t *xc, const float *sx, int32_t x_rows,
+                    const int32_t *perm, int32_t topk, int32_t R_max, const int32_t *seg, fq_shape s,
+                    const fq_stored_w *w, uint16_t *out, fq_stream stream) {
+  FQ_TRY(check_product(xc, x_rows, perm, topk, R_max, seg, s, gated, 1, out));
+  FQ_TRY(check_int8_w(w, s));
+  FQ_CHECK_ARG(R_max == 0 || (sx && (reinterpret_cast<uintptr_t>(sx) & 3u) == 0),
+               "x_scale must be non-NULL, 4-byte aligned");
+  if (R_max == 0) return FQ_OK;
+  launch_int8_product(xc, sx, perm, topk, R_max, seg, s, *w, gated, out, S(stream));
+  FQ_CHECK_LAUNCH(fn);
+  return FQ_OK;
+}
+
+// The tensors that the norm's forward and backward share.
+fq_status check_norm(int32_t T, int32_t H, const uint16_t *b, const float *gate, float alpha,
+                     const uint16_t *w_post, const uint16_t *w_pre, float eps) {
+  FQ_CHECK_ARG(T >= 0 && H > 0 && H % 16 == 0, "bad sizes (T=%d H=%d; H %% 16 == 0)", T, H);
+  FQ_CHECK_SUPPORTED(H <= kNormMaxRow, "rows of up to %d elements (H=%d)", kNormMaxRow, H);
+  FQ_CHECK_ARG(eps > 0.0f && eps <= 3.4028235e38f, "eps must be finite and > 0");
+  FQ_CHECK_ARG(alpha - alpha == 0.0f, "alpha must be finite");
+  FQ_CHECK_ARG(b || (!gate && !w_post), "gate and w_post belong to a block output b");
+  FQ_CHECK_ARG((!b || aligned16(b)) && (!w_post || aligned16(w_post)) && (!w_pre || aligned16(w_pre)),
+               "bf16 tensors must be 16-byte aligned");
+  return FQ_OK;
+}
+
 }  // namespace
 }  // namespace fq
 
@@ -249,6 +312,10 @@ size_t fq_workspace_bytes(int32_t op, fq_shape shape, int32_t R_max, int32_t fmt
     if (fmts <= 0 || R_max < 0 || R_max % fmts || shape.E <= 0 || shape.N <= 0 || shape.K <= 0)
       return 0;
     return moe_tokens_ws_bytes(R_max / fmts, fmts, shape.E, shape.K);
+  }
+  if (op == FQ_OP_NORM) {
+    if (shape.N < 0 || shape.K <= 0) return 0;
+    return align_up(norm_ws_bytes(shape.N, shape.K));
   }
   return 0;
 }
@@ -904,6 +971,121 @@ fq_status fq_swiglu_bwd_ckpt(const uint16_t *daq, const uint8_t *codes, const fl
                          aq ? aq->scale : nullptr, dh, aqo, dscale_a, static_cast<float *>(ws),
                          S(stream));
   FQ_CHECK_LAUNCH("fq_swiglu_bwd_ckpt");
+  return FQ_OK;
+}
+
+fq_status fq_quantize_tokens(const uint16_t *x, int32_t rows, int32_t K, const int32_t *n_rows,
+                             uint8_t *codes, float *scale, fq_stream stream) {
+  FQ_CHECK_ARG(rows >= 0 && K > 0 && K % 16 == 0, "bad sizes (rows=%d K=%d; K %% 16 == 0)", rows, K);
+  FQ_CHECK_ARG(rows == 0 || (x && codes && scale), "NULL pointer");
+  FQ_CHECK_ARG((!x || aligned16(x)) && (!codes || aligned16(codes)),
+               "x and codes must be 16-byte aligned");
+  FQ_CHECK_ARG((reinterpret_cast<uintptr_t>(scale) & 3u) == 0, "scale must be 4-byte aligned");
+  if (rows == 0) return FQ_OK;
+  launch_quantize_tokens(x, rows, K, n_rows, codes, scale, S(stream));
+  FQ_CHECK_LAUNCH("fq_quantize_tokens");
+  return FQ_OK;
+}
+
+fq_status fq_grouped_gemm_int8(const uint8_t *x_codes, const float *x_scale, int32_t x_rows,
+                               const int32_t *perm, int32_t topk, int32_t R_max, const int32_t *seg,
+                               fq_shape s, const fq_stored_w *w, uint16_t *y, void *ws,
+                               size_t ws_bytes, fq_stream stream) {
+  (void)ws;
+  (void)ws_bytes;
+  return int8_call("fq_grouped_gemm_int8", false, x_codes, x_scale, x_rows, perm, topk, R_max, seg, s, w,
+                   y, stream);
+}
+
+fq_status fq_grouped_gated_int8(const uint8_t *x_codes, const float *x_scale, int32_t x_rows,
+                                const int32_t *perm, int32_t topk, int32_t R_max, const int32_t *seg,
+                                fq_shape s, const fq_stored_w *w, uint16_t *a, void *ws,
+                                size_t ws_bytes, fq_stream stream) {
+  (void)ws;
+  (void)ws_bytes;
+  return int8_call("fq_grouped_gated_int8", true, x_codes, x_scale, x_rows, perm, topk, R_max, seg, s, w,
+                   a, stream);
+}
+
+fq_status fq_grouped_gated_fwd(const uint16_t *x, int32_t x_rows, const int32_t *perm, int32_t topk,
+                               int32_t R_max, const int32_t *seg, fq_shape s, const uint16_t *w_fq,
+                               const fq_act_q *aq, uint16_t *aqo, void *ws, size_t ws_bytes,
+                               fq_stream stream) {
+  (void)ws;
+  (void)ws_bytes;
+  FQ_TRY(check_product(x, x_rows, perm, topk, R_max, seg, s, true, 2, aqo));
+  FQ_CHECK_ARG(w_fq && aligned16(w_fq), "w_fq must be non-NULL, 16-byte aligned");
+  FQ_TRY(check_act_q(aq, s.N / 2));
+  if (R_max == 0) return FQ_OK;
+  launch_gated(nullptr, x, perm, topk, R_max, seg, s, w_fq, act_fmt(aq), aq ? aq->scale : nullptr, aqo,
+               nullptr, S(stream));
+  FQ_CHECK_LAUNCH("fq_grouped_gated_fwd");
+  return FQ_OK;
+}
+
+fq_status fq_grouped_gated_bwd(const uint16_t *daq, const uint16_t *x, int32_t x_rows,
+                               const int32_t *perm, int32_t topk, int32_t R_max, const int32_t *seg,
+                               fq_shape s, const uint16_t *w_fq, const fq_act_q *aq, uint16_t *dh,
+                               uint16_t *aqo, void *ws, size_t ws_bytes, fq_stream stream) {
+  (void)ws;
+  (void)ws_bytes;
+  FQ_TRY(check_product(x, x_rows, perm, topk, R_max, seg, s, true, 2, dh));
+  FQ_CHECK_ARG(R_max == 0 || daq, "daq is NULL");
+  FQ_CHECK_ARG((!daq || aligned16(daq)) && (!aqo || aligned16(aqo)) && w_fq && aligned16(w_fq),
+               "w_fq must be non-NULL, bf16 tensors 16-byte aligned");
+  FQ_TRY(check_act_q(aq, s.N / 2));
+  if (R_max == 0) return FQ_OK;
+  launch_gated(daq, x, perm, topk, R_max, seg, s, w_fq, act_fmt(aq), aq ? aq->scale : nullptr, dh, aqo,
+               S(stream));
+  FQ_CHECK_LAUNCH("fq_grouped_gated_bwd");
+  return FQ_OK;
+}
+
+fq_status fq_norm_residual_fwd(const uint16_t *x, const uint16_t *b, const float *gate, float alpha,
+                               const uint16_t *w_post, const uint16_t *w_pre, float eps, int32_t T,
+                               int32_t H, uint16_t *y, uint16_t *n, uint8_t *codes, float *scale,
+                               fq_stream stream) {
+  FQ_TRY(check_norm(T, H, b, gate, alpha, w_post, w_pre, eps));
+  FQ_CHECK_ARG(T == 0 || x, "x is NULL");
+  FQ_CHECK_ARG(y || n || codes, "no output");
+  FQ_CHECK_ARG(w_pre || (!n && !codes), "n and codes need w_pre");
+  FQ_CHECK_ARG(!w_pre || n || codes, "w_pre needs n or codes");
+  FQ_CHECK_ARG(!codes == !scale, "codes and scale go together");
+  FQ_CHECK_ARG((!x || aligned16(x)) && (!y || aligned16(y)) && (!n || aligned16(n)) &&
+                   (!codes || aligned16(codes)) && (reinterpret_cast<uintptr_t>(scale) & 3u) == 0,
+               "tensors must be 16-byte aligned (scale: 4)");
+  if (T == 0) return FQ_OK;
+  launch_norm_fwd(x, b, gate, alpha, w_post, w_pre, eps, T, H, y, n, codes, scale, S(stream));
+  FQ_CHECK_LAUNCH("fq_norm_residual_fwd");
+  return FQ_OK;
+}
+
+fq_status fq_norm_residual_bwd(const uint16_t *dy, const uint16_t *dn, const uint16_t *y,
+                               const uint16_t *b, const float *gate, float alpha,
+                               const uint16_t *w_post, const uint16_t *w_pre, float eps, int32_t T,
+                               int32_t H, uint16_t *dx, uint16_t *db, float *dgate, float *dw_post,
+                               float *dw_pre, void *ws, size_t ws_bytes, fq_stream stream) {
+  FQ_TRY(check_norm(T, H, b, gate, alpha, w_post, w_pre, eps));
+  FQ_CHECK_ARG(dx || db || dgate || dw_post || dw_pre, "no output");
+  FQ_CHECK_ARG(dy || dn || T == 0, "dy and dn are both NULL");
+  FQ_CHECK_ARG(!dn || (y && w_pre) || T == 0, "dn needs y and w_pre");
+  FQ_CHECK_ARG(!dw_pre || w_pre, "dw_pre needs w_pre");
+  FQ_CHECK_ARG(!dw_pre || dn || T == 0, "dw_pre needs dn");
+  FQ_CHECK_ARG(b || T == 0 || (!db && !dgate && !dw_post), "db, dgate and dw_post need b");
+  FQ_CHECK_ARG(!dw_post || w_post, "dw_post needs w_post");
+  FQ_CHECK_ARG(!dgate || gate, "dgate needs gate");
+  FQ_CHECK_ARG((!dy || aligned16(dy)) && (!dn || aligned16(dn)) && (!y || aligned16(y)) &&
+                   (!dx || aligned16(dx)) && (!db || aligned16(db)),
+               "bf16 tensors must be 16-byte aligned");
+  const size_t need = dw_post || dw_pre ? align_up(norm_ws_bytes(T, H)) : 0;
+  if (need > 0 && (!ws || ws_bytes < need)) {
+    set_error("fq_norm_residual_bwd: workspace %zu bytes < %zu needed", ws_bytes, need);
+    return FQ_ERR_WORKSPACE_TOO_SMALL;
+  }
+  FQ_CHECK_ARG(need == 0 || aligned16(ws), "the workspace must be 16-byte aligned");
+  launch_norm_bwd(dy, dn, y, b, gate, alpha, w_post, w_pre, eps, T, H, dx, db, dgate, dw_post, dw_pre,
+                  static_cast<float *>(ws), S(stream));
+  FQ_CHECK_LAUNCH("fq_norm_residual_bwd");
   return FQ_OK;
 }
 

@@ -95,6 +95,29 @@ void launch_validate(const int32_t *ids, long n_ids, int n_experts, const int32_
                      const float *zero_point, const float *gscale, int n_g, const float *act_scale,
                      uint32_t *status, hipStream_t st);
 
+// int8 codes of token rows with one scale a row (fq_quantize_tokens)
+void launch_quantize_tokens(const uint16_t *x, int rows, int K, const int32_t *n_rows, uint8_t *codes,
+                            float *scale, hipStream_t st);
+// Products with int8 operands (gated: gate and up rows, SwiGLU) and the bf16 gated
+// block; perm / topk as for launch_gemm_fwd. daq: the backward (out = dh, aq may be NULL).
+constexpr int kInt8MaxK = 131071;  // 128 * 128 * K fits an int32 sum
+void launch_int8_product(const uint8_t *xc, const float *sx, const int32_t *perm, int topk, int R_max,
+                         const int32_t *seg, fq_shape s, const fq_stored_w &w, bool gated,
+                         uint16_t *out, hipStream_t st);
+void launch_gated(const uint16_t *daq, const uint16_t *x, const int32_t *perm, int topk, int R_max,
+                  const int32_t *seg, fq_shape s, const uint16_t *w, int afmt, const float *ascale,
+                  uint16_t *out, uint16_t *aq, hipStream_t st);
+// norms around a block; rows up to kNormWaveRow lie in one wave, up to kNormMaxRow in four
+constexpr int kNormWaveRow = 2048, kNormMaxRow = 16384;
+size_t norm_ws_bytes(int T, int H);
+void launch_norm_fwd(const uint16_t *x, const uint16_t *b, const float *gate, float alpha,
+                     const uint16_t *w_post, const uint16_t *w_pre, float eps, int T, int H,
+                     uint16_t *y, uint16_t *n, uint8_t *codes, float *scale, hipStream_t st);
+void launch_norm_bwd(const uint16_t *dy, const uint16_t *dn, const uint16_t *y, const uint16_t *b,
+                     const float *gate, float alpha, const uint16_t *w_post, const uint16_t *w_pre,
+                     float eps, int T, int H, uint16_t *dx, uint16_t *db, float *dgate,
+                     float *dw_post, float *dw_pre, float *ws, hipStream_t st);
+
 size_t permute_workspace_bytes(int E, long P);
 // Size of the permute scratch array the allocation-free entry point uses.
 constexpr size_t kPermuteScratchBytes = size_t(4) << 20;
