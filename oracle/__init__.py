@@ -88,3 +88,7 @@ from .ckpt import (  # noqa: F401
     CKPT_D, ckpt_save, ckpt_load, ckpt_values, swiglu_from_values, swiglu_bwd_values, a_bits_of,
 )
 from .moe_tokens import moe_tokens, stored_values  # noqa: F401
+from .blocks import (  # noqa: F401
+    quantize_tokens, int8_sums, gemm_int8, gated_sums, gated, gated_bwd, norm_residual,
+    norm_residual_bwd,
+)
