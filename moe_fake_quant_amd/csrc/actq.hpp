@@ -63,10 +63,11 @@ __device__ __forceinline__ uint32_t act_fq16(const ActQ &q, float *x) {
   return mask;
 }
 
-// 8 consecutive elements along K, one half of a 16-element block; the other
-// half is on lane ^ 1, which must run the same call (NVFP4 takes the block
-// amax over both halves, so the result equals act_fq16 on the whole block).
-// Values in place, 8 mask bits out.
+// 8 elements along K, one half of a 16-element block; the other half is on
+// lane ^ PARTNER, which must run the same call (NVFP4 takes the block amax over
+// both halves, so the result equals act_fq16 on the whole block). Values in
+// place, 8 mask bits out.
+template <int PARTNER = 1>
 __device__ __forceinline__ uint32_t act_fq8_pair(const ActQ &q, float *x) {
   uint32_t mask = 0;
   if (q.fmt == FQ_FMT_NONE) return 0xFFu;
@@ -77,7 +78,7 @@ __device__ __forceinline__ uint32_t act_fq8_pair(const ActQ &q, float *x) {
       float amax = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
-      amax = fmaxf(amax, __shfl_xor(amax, 1, 64));
+      amax = fmaxf(amax, __shfl_xor(amax, PARTNER, 64));
       s = nvfp4_dynamic_scale(amax, q.s);
       if (s == 0.0f) {  // zero block: +0.0, mask 0
 #pragma unroll

@@ -126,6 +126,9 @@ fq_status permute_scratch(int32_t **out);
 void launch_permute(const int32_t *ids, int T, int topk, int ebegin, int E, int32_t *perm,
                     int32_t *row_of, int32_t *seg, void *ws, hipStream_t st);
 
+// the current device's CU count rounded down to a multiple of 8 (the XCD count)
+int device_cus();
+
 // xperm / topk: routed row r of X is row xperm[r] / topk of a token-indexed
 // xq (FWD's X operand, WGRAD's X operand); NULL = xq indexed by routed row.
 // part: fp32 scratch of gemm_ksplit_bytes for a call small enough to split

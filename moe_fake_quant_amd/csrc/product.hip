@@ -13,38 +13,15 @@
 // MFMA operand is 16 bytes a lane for bf16 (16x16x32) and int8 (16x16x64) alike,
 // so both types share the loads.
 #include "internal.hpp"
+#include "product.hpp"
 #include "rowq.hpp"
+#include "tile.hpp"
 
 namespace fq {
 
 namespace {
 
-typedef __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16 bf16x8v;
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-enum Kind { PLAIN = 0, GATED = 1, GATED_BWD = 2 };
-
-struct ProdArgs {
-  const char *w, *x;       // weights [E, N, KB], x rows of KB bytes
-  const int32_t *perm;     // x row of routed row r is perm[r] / topk; NULL: r
-  FastDiv topk;
-  const int32_t *seg;      // [E + 1]
-  int E, N;                // weight rows of an expert (gated: 2F)
-  int C;                   // output columns (N, gated: F)
-  uint32_t KB;             // bytes of a row
-  const float *sx, *sw;    // int8: token scales, channel scales
-  int sw_rows;             // 1: sw [E, N], 0: sw [E]
-  const uint16_t *daq;     // bwd [R, F]
-  int afmt;
-  const float *ascale;
-  uint16_t *out;           // y, aq or dh
-  uint16_t *aq;            // bwd: FQ_a(a), or NULL
-};
-
-__device__ __forceinline__ int x_row(const ProdArgs &a, int r) {
-  return a.perm ? (int)a.topk.div((uint32_t)a.perm[r]) : r;
-}
 
 // The outputs of 8 columns c0 .. c0+7 of row r from their sums (g, and u for the
 // gated kinds). Lane ^ 1 holds the other half of the 16-block and runs the same
@@ -71,8 +48,7 @@ __device__ __forceinline__ void finish8(const ProdArgs &a, const ActQ &q, int r,
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float da = (m >> j) & 1u ? d[j] : 0.0f;
-        dg[j] = ((da * u[j]) * sig[j]) * (1.0f + g[j] * (1.0f - sig[j]));
-        du[j] = (da * g[j]) * sig[j];
+        swiglu_grad(da, g[j], u[j], sig[j], dg[j], du[j]);
       }
       uint16_t *o = a.out + (size_t)r * 2 * a.C + c0;
       *reinterpret_cast<bf16x8_t *>(o) = pack8(dg);
@@ -203,8 +179,15 @@ __global__ __launch_bounds__(NW * 64) void k_rows_product(ProdArgs a) {
 
 }  // namespace
 
+// rows of an expert, were they spread evenly, from which the tiles are taken
+constexpr int kTileRows = 64;
+
 template <int KIND, bool I8>
-static void launch_rows(const ProdArgs &a, int R_max, hipStream_t st) {
+static void launch_product(const ProdArgs &a, int R_max, hipStream_t st) {
+  if ((R_max + a.E - 1) / a.E > kTileRows) {
+    launch_tile_product(a, KIND, I8, R_max, st);
+    return;
+  }
   // rows of an expert, were they spread evenly
   const int per = (R_max + a.E - 1) / a.E;
   const int mt = per <= 16 ? 1 : per <= 32 ? 2 : 4;
@@ -239,8 +222,8 @@ void launch_int8_product(const uint8_t *xc, const float *sx, const int32_t *perm
   a.sw = w.scale;
   a.sw_rows = w.group != FQ_GROUP_TENSOR;
   a.out = out;
-  if (gated) launch_rows<GATED, true>(a, R_max, st);
-  else launch_rows<PLAIN, true>(a, R_max, st);
+  if (gated) launch_product<GATED, true>(a, R_max, st);
+  else launch_product<PLAIN, true>(a, R_max, st);
 }
 
 void launch_gated(const uint16_t *daq, const uint16_t *x, const int32_t *perm, int topk, int R_max,
@@ -252,8 +235,8 @@ void launch_gated(const uint16_t *daq, const uint16_t *x, const int32_t *perm, i
   a.ascale = ascale;
   a.out = out;
   a.aq = aq;
-  if (daq) launch_rows<GATED_BWD, false>(a, R_max, st);
-  else launch_rows<GATED, false>(a, R_max, st);
+  if (daq) launch_product<GATED_BWD, false>(a, R_max, st);
+  else launch_product<GATED, false>(a, R_max, st);
 }
 
 }  // namespace fq
