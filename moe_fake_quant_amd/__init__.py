@@ -5,8 +5,9 @@ kernels; torch provides device memory and the current stream).
 Each function has the name and argument order of its C entry point in
 include/fq.h, takes device tensors (or None for a NULL pointer), enqueues on
 ``torch.cuda.current_stream()`` and raises ``FQError`` for a non-OK status.
-Importing this package loads ``libfq.so`` from this directory and fails
-loudly when it is missing; there is no fallback.
+Importing this package loads ``libfq.so`` and ``_fqbind.so`` (the native
+marshalling of the calls whose kernels are short) from this directory and fails
+loudly when one is missing; there is no fallback.
 """
 from __future__ import annotations
 
@@ -161,6 +162,8 @@ def _load() -> ctypes.CDLL:
 
 _lib = _load()
 
+from . import _fqbind as _b  # noqa: E402  (built next to libfq.so, which it links)
+
 
 def lib() -> ctypes.CDLL:
     return _lib
@@ -196,13 +199,12 @@ def _stream():
     return _raw_stream(torch.cuda.current_device())
 
 
-def _same_device(*tensors: Optional[torch.Tensor]):
+def _same_device(t: Optional[torch.Tensor]):
     """The calls run on the current device's stream; its kernels must not be
     handed another device's memory."""
-    for t in tensors:
-        if t is not None and t.is_cuda and t.get_device() != torch.cuda.current_device():
-            raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
+    if t is not None and t.is_cuda and t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
 
 
 @dataclasses.dataclass
@@ -422,58 +424,46 @@ def fq_topk_kl(student, teacher, T, V, K, reverse, valid, topk_idx, grad, loss_t
                            _nbytes(ws), _stream()))
 
 
+# The calls below are marshalled natively (bind/bind.cpp): contiguous device tensors
+# on the current device, or None; shape (E, N, K).
+
 def fq_quantize_tokens(x, rows, K, n_rows, codes, scale):
-    _same_device(x, codes, scale)
-    _check(_lib.fq_quantize_tokens(_p(x), int(rows), int(K), _p(n_rows), _p(codes), _p(scale),
-                                   _stream()))
+    _check(_b.fq_quantize_tokens(x, rows, K, n_rows, codes, scale))
 
 
 def fq_grouped_gemm_int8(x_codes, x_scale, x_rows, perm, topk, R_max, seg_offsets, shape, w: StoredW,
                          y, ws=None):
-    _same_device(x_codes, w.codes, y, ws)
-    _check(_lib.fq_grouped_gemm_int8(_p(x_codes), _p(x_scale), int(x_rows), _p(perm), int(topk),
-                                     int(R_max), _p(seg_offsets), _shape(*shape),
-                                     ctypes.byref(w.c()), _p(y), _p(ws), _nbytes(ws), _stream()))
+    _check(_b.fq_grouped_gemm_int8(x_codes, x_scale, x_rows, perm, topk, R_max, seg_offsets, shape, w,
+                                   y, ws))
 
 
 def fq_grouped_gated_int8(x_codes, x_scale, x_rows, perm, topk, R_max, seg_offsets, shape, w: StoredW,
                           a, ws=None):
-    _same_device(x_codes, w.codes, a, ws)
-    _check(_lib.fq_grouped_gated_int8(_p(x_codes), _p(x_scale), int(x_rows), _p(perm), int(topk),
-                                      int(R_max), _p(seg_offsets), _shape(*shape),
-                                      ctypes.byref(w.c()), _p(a), _p(ws), _nbytes(ws), _stream()))
+    _check(_b.fq_grouped_gated_int8(x_codes, x_scale, x_rows, perm, topk, R_max, seg_offsets, shape, w,
+                                    a, ws))
 
 
 def fq_grouped_gated_fwd(x, x_rows, perm, topk, R_max, seg_offsets, shape, w_fq, aq: Optional[ActQ],
                          aq_out, ws=None):
-    _same_device(x, w_fq, aq_out, ws)
-    _check(_lib.fq_grouped_gated_fwd(_p(x), int(x_rows), _p(perm), int(topk), int(R_max),
-                                     _p(seg_offsets), _shape(*shape), _p(w_fq), _aq(aq), _p(aq_out),
-                                     _p(ws), _nbytes(ws), _stream()))
+    _check(_b.fq_grouped_gated_fwd(x, x_rows, perm, topk, R_max, seg_offsets, shape, w_fq, aq, aq_out,
+                                   ws))
 
 
 def fq_grouped_gated_bwd(daq, x, x_rows, perm, topk, R_max, seg_offsets, shape, w_fq,
                          aq: Optional[ActQ], dh, aq_out=None, ws=None):
-    _same_device(daq, x, w_fq, dh, ws)
-    _check(_lib.fq_grouped_gated_bwd(_p(daq), _p(x), int(x_rows), _p(perm), int(topk), int(R_max),
-                                     _p(seg_offsets), _shape(*shape), _p(w_fq), _aq(aq), _p(dh),
-                                     _p(aq_out), _p(ws), _nbytes(ws), _stream()))
+    _check(_b.fq_grouped_gated_bwd(daq, x, x_rows, perm, topk, R_max, seg_offsets, shape, w_fq, aq, dh,
+                                   aq_out, ws))
 
 
 def fq_norm_residual_fwd(x, b, gate, alpha, w_post, w_pre, eps, T, H, y=None, n=None, codes=None,
                          scale=None):
-    _same_device(x, b, y, n, codes)
-    _check(_lib.fq_norm_residual_fwd(_p(x), _p(b), _p(gate), float(alpha), _p(w_post), _p(w_pre),
-                                     float(eps), int(T), int(H), _p(y), _p(n), _p(codes), _p(scale),
-                                     _stream()))
+    _check(_b.fq_norm_residual_fwd(x, b, gate, alpha, w_post, w_pre, eps, T, H, y, n, codes, scale))
 
 
 def fq_norm_residual_bwd(dy, dn, y, b, gate, alpha, w_post, w_pre, eps, T, H, dx=None, db=None,
                          dgate=None, dw_post=None, dw_pre=None, ws=None):
-    _same_device(dy, dn, y, b, dx, db, ws)
-    _check(_lib.fq_norm_residual_bwd(_p(dy), _p(dn), _p(y), _p(b), _p(gate), float(alpha), _p(w_post),
-                                     _p(w_pre), float(eps), int(T), int(H), _p(dx), _p(db), _p(dgate),
-                                     _p(dw_post), _p(dw_pre), _p(ws), _nbytes(ws), _stream()))
+    _check(_b.fq_norm_residual_bwd(dy, dn, y, b, gate, alpha, w_post, w_pre, eps, T, H, dx, db, dgate,
+                                   dw_post, dw_pre, ws))
 
 
 from .layer import MoEFakeQuantLayer  # noqa: E402,F401

@@ -730,8 +730,9 @@ fq_status gemm_bwd_call(const char *fn, const uint16_t *dy, const uint16_t *x, i
     wfq_p = c.take<uint16_t>((size_t)s.E * p.N * p.K * 2);
     launch_reshape_u16(wfq, s.E, s.N, s.K, wfq_p, p.N, p.K, nullptr, st);
   }
+  // the raw weights and the scales only enter dScale
   uint16_t *w_p = c.take<uint16_t>((size_t)s.E * p.N * p.K * 2);
-  launch_reshape_u16(w, s.E, s.N, s.K, w_p, p.N, p.K, nullptr, st);
+  if (want_ds) launch_reshape_u16(w, s.E, s.N, s.K, w_p, p.N, p.K, nullptr, st);
   uint16_t *x_p = c.take<uint16_t>((size_t)x_rows * p.K * 2);
   uint16_t *dy_p = c.take<uint16_t>((size_t)R_max * p.N * 2);
   uint16_t *dx_p = c.take<uint16_t>((size_t)R_max * p.K * 2);
@@ -743,7 +744,7 @@ fq_status gemm_bwd_call(const char *fn, const uint16_t *dy, const uint16_t *x, i
   float *ds_p = c.take<float>(nsc), *dzp_p = c.take<float>(nsc);
   fq_weight_q wq_p = *wq;
   wq_p.group = group_p;
-  if (!per_tensor) {
+  if (!per_tensor && want_ds) {
     launch_reshape_f32(wq->scale, s.E, s.N, G, sc_p, p.N, Gp,
                        wq->fmt == FQ_FMT_NVFP4 ? 0.0f : 1.0f, st);
     wq_p.scale = sc_p;

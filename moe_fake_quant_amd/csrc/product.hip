@@ -14,7 +14,6 @@
 // so both types share the loads.
 #include "internal.hpp"
 #include "product.hpp"
-#include "rowq.hpp"
 #include "tile.hpp"
 
 namespace fq {
@@ -22,40 +21,6 @@ namespace fq {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-// The outputs of 8 columns c0 .. c0+7 of row r from their sums (g, and u for the
-// gated kinds). Lane ^ 1 holds the other half of the 16-block and runs the same
-// call; `store` says whether this lane's row exists.
-template <int KIND>
-__device__ __forceinline__ void finish8(const ProdArgs &a, const ActQ &q, int r, int c0, float *g,
-                                        const float *u, bool store) {
-  if constexpr (KIND == PLAIN) {
-    if (store) *reinterpret_cast<bf16x8_t *>(a.out + (size_t)r * a.C + c0) = pack8(g);
-  } else {
-    float v[8], sig[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      sig[j] = sigmoid_hw(g[j]);
-      v[j] = bf16_to_f32(f32_to_bf16((g[j] * sig[j]) * u[j]));
-    }
-    const uint32_t m = act_fq8_pair(q, v);
-    if constexpr (KIND == GATED) {
-      if (store) *reinterpret_cast<bf16x8_t *>(a.out + (size_t)r * a.C + c0) = pack8(v);
-    } else if (store) {
-      if (a.aq) *reinterpret_cast<bf16x8_t *>(a.aq + (size_t)r * a.C + c0) = pack8(v);
-      float d[8], dg[8], du[8];
-      unpack8(*reinterpret_cast<const bf16x8_t *>(a.daq + (size_t)r * a.C + c0), d);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float da = (m >> j) & 1u ? d[j] : 0.0f;
-        swiglu_grad(da, g[j], u[j], sig[j], dg[j], du[j]);
-      }
-      uint16_t *o = a.out + (size_t)r * 2 * a.C + c0;
-      *reinterpret_cast<bf16x8_t *>(o) = pack8(dg);
-      *reinterpret_cast<bf16x8_t *>(o + a.C) = pack8(du);
-    }
-  }
-}
 
 template <bool I8>
 __device__ __forceinline__ void mfma16(const i32x4 &w, const i32x4 &x, i32x4 &acc) {
@@ -70,66 +35,77 @@ __device__ __forceinline__ void mfma16(const i32x4 &w, const i32x4 &x, i32x4 &ac
 }
 
 // Few rows: the weights' stream bounds it. A block takes 16 output columns of one
-// expert and MT * 16 rows; its NW waves share out the contraction in pieces of 256
-// bytes, read both operands from global memory straight into MFMA fragments, and
-// leave their sums in LDS, where they are added in wave order.
-// Grid: (columns / 16, E, row chunks, strided).
-constexpr int NW = 8;
-template <int KIND, bool I8, int MT>
+// expert and MT * 16 rows; its waves share out the contraction in pieces of U * 64
+// bytes, read both operands from global memory straight into MFMA fragments, the
+// next piece's before this one's are multiplied, and leave their sums in LDS, where
+// they are added in wave order. Grid: (columns / 16, E, row chunks, strided).
+template <int KIND, bool I8, int MT, int NW>
 __global__ __launch_bounds__(NW * 64) void k_rows_product(ProdArgs a) {
   constexpr int NP = KIND == PLAIN ? 1 : 2;   // gate and up
+  constexpr int U = MT > 2 ? 2 : 4;
   constexpr int S = NP * MT * 256;            // sums of a block
   __shared__ __attribute__((aligned(16))) int part[NW * S];
   const int e = blockIdx.y, c0 = blockIdx.x * 16;
-  const int r_end = a.seg[e + 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, kq = (lane >> 4) * 16;
-  const ActQ q = load_actq(KIND == PLAIN ? FQ_FMT_NONE : a.afmt, a.ascale);
+  struct Piece {
+    i32x4 w[NP][U], x[MT][U];
+  };
   const char *wrow[NP];
 #pragma unroll
   for (int p = 0; p < NP; ++p)
     wrow[p] = a.w + ((size_t)e * a.N + (size_t)p * a.C + c0 + l16) * a.KB;
+  // the last piece may end inside: chunks past the row's end are zero in both operands
+  auto load_w = [&](Piece &d, uint32_t k0) {
+#pragma unroll
+    for (int s = 0; s < U; ++s) {
+      const uint32_t k = k0 + 64 * s + kq;
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+        d.w[p][s] = k < a.KB ? *reinterpret_cast<const i32x4 *>(wrow[p] + k) : i32x4{0, 0, 0, 0};
+    }
+  };
+  const uint32_t first = U * 64 * wave;
+  Piece cur;
+  // one expert: its weights are on the way before the row count is known
+  if (gridDim.y == 1) load_w(cur, first);
+  const int r_end = a.seg[e + 1];
+  const ActQ q = load_actq(KIND == PLAIN ? FQ_FMT_NONE : a.afmt, a.ascale);
   for (int r0 = a.seg[e] + blockIdx.z * (16 * MT); r0 < r_end; r0 += gridDim.z * (16 * MT)) {
     const char *xrow[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
       xrow[m] = a.x + (size_t)x_row(a, min(r0 + 16 * m + l16, r_end - 1)) * a.KB;
+    auto load_x = [&](Piece &d, uint32_t k0) {
+#pragma unroll
+      for (int s = 0; s < U; ++s) {
+        const uint32_t k = k0 + 64 * s + kq;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          d.x[m][s] = k < a.KB ? *reinterpret_cast<const i32x4 *>(xrow[m] + k) : i32x4{0, 0, 0, 0};
+      }
+    };
     i32x4 acc[NP][MT];
 #pragma unroll
     for (int p = 0; p < NP; ++p)
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[p][m] = i32x4{0, 0, 0, 0};
-    // a piece of 256 bytes; the last one may end inside: chunks past the row's end
-    // are zero in both operands
-    auto piece = [&](uint32_t k0, auto tail_tag) {
-      constexpr bool TAIL = decltype(tail_tag)::value;
-      i32x4 w[NP][4], x[MT][4];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const uint32_t k = k0 + 64 * s + kq;
-        const bool in = !TAIL || k < a.KB;
-        const uint32_t at = in ? k : 0;
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          w[p][s] = *reinterpret_cast<const i32x4 *>(wrow[p] + at);
-          if (!in) w[p][s] = i32x4{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          x[m][s] = *reinterpret_cast<const i32x4 *>(xrow[m] + at);
-          if (!in) x[m][s] = i32x4{0, 0, 0, 0};
-        }
+    if (gridDim.y != 1 || r0 != a.seg[e] + blockIdx.z * (16 * MT)) load_w(cur, first);
+    load_x(cur, first);
+    for (uint32_t k0 = first; k0 < a.KB; k0 += U * 64 * NW) {
+      Piece next;
+      if (k0 + U * 64 * NW < a.KB) {
+        load_w(next, k0 + U * 64 * NW);
+        load_x(next, k0 + U * 64 * NW);
       }
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int s = 0; s < U; ++s)
 #pragma unroll
         for (int p = 0; p < NP; ++p)
 #pragma unroll
-          for (int m = 0; m < MT; ++m) mfma16<I8>(w[p][s], x[m][s], acc[p][m]);
-    };
-    uint32_t k0 = 256 * wave;
-    for (; k0 + 256 <= a.KB; k0 += 256 * NW) piece(k0, std::false_type{});
-    if (k0 < a.KB) piece(k0, std::true_type{});
+          for (int m = 0; m < MT; ++m) mfma16<I8>(cur.w[p][s], cur.x[m][s], acc[p][m]);
+      cur = next;
+    }
     // acc[p][m] of this lane: columns c0 + 4 (lane / 16) + v, row r0 + 16 m + lane % 16
 #pragma unroll
     for (int p = 0; p < NP; ++p)
@@ -160,16 +136,7 @@ __global__ __launch_bounds__(NW * 64) void k_rows_product(ProdArgs a) {
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
         const int *src = part + (p * MT + (j >> 4)) * 256 + (j & 15) * 16 + half;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if constexpr (I8) {
-            const size_t n = (size_t)e * a.N + (size_t)p * a.C + c0 + half + k;
-            const float sx = a.sx[x_row(a, live ? r : r_end - 1)];
-            v[p][k] = ((float)src[k] * sx) * a.sw[a.sw_rows ? n : (size_t)e];
-          } else {
-            v[p][k] = __int_as_float(src[k]);
-          }
-        }
+        sums8<I8>(a, e, live ? r : r_end - 1, p * a.C + c0 + half, src, v[p]);
       }
       finish8<KIND>(a, q, r, c0 + half, v[0], v[NP - 1], live);
     }
@@ -179,24 +146,50 @@ __global__ __launch_bounds__(NW * 64) void k_rows_product(ProdArgs a) {
 
 }  // namespace
 
-// rows of an expert, were they spread evenly, from which the tiles are taken
-constexpr int kTileRows = 64;
+// The form of a call, by the work units that R_max rows spread evenly over the experts
+// would give. us of one call on 256 CUs, int8 / gated int8 / gated bf16, bf16 backward:
+//   rows a expert       few rows          64 x 64         128 x 128        256 x 256
+//   one [4096 x 4096]
+//     16               8 / 9 / 14, 15   12 / 12 / 19, 19  23 / 24 / 43, 44  37 / 48 / 67, 89
+//     64              13 / 16 / 26, 27  12 / 12 / 20, 21  21 / 20 / 30, 32  37 / 48 / 68, 91
+//     512             87 / 55 / 94, 97  19 / 18 / 30, 33  25 / 23 / 32, 37  45 / 60 / 84, 110
+//     1024                              33 / 32 / 58, 61  29 / 27 / 40, 43  46 / 60 / 84, 111
+//     2048                              64 / 61 / 110, 117  51 / 43 / 69, 73  49 / 61 / 85, 113
+//     4096                              126 / 121 / 236, 258  92 / 83 / 138, 149  64 / 69 / 112, 133
+//   128 of [1536 x 2048]
+//     16            121 / 131 / 211, 227  87 / 82 / 147, 155  92 / 88 / 154, 159  91 / 111 / 165, 205
+//     128                               154 / 146 / 249, 260  143 / 114 / 202, 233  105 / 120 / 175, 233
+//     256                               264 / 252 / 421, 445  229 / 185 / 275, 308  132 / 141 / 216, 291
+enum Form { kRows, kMid64, kMid128, kTile256 };
+
+static Form pick_form(const ProdArgs &a, int kind, int R_max) {
+  const int64_t cus = device_cus(), per = (R_max + a.E - 1) / a.E;
+  auto units = [&](int64_t tile) {
+    const int64_t cols = kind == PLAIN ? tile : tile / 2;
+    return (a.C + cols - 1) / cols * a.E * ((per + tile - 1) / tile);
+  };
+  // blocks of 16 columns and up to 64 rows: two rounds of them at most for up to 32 rows
+  // an expert, one beyond
+  const int64_t blocks = (int64_t)(a.C / 16) * a.E * ((per + 63) / 64);
+  if (blocks <= (per <= 32 ? 2 * cus : cus)) return kRows;
+  if (per > 64 && units(256) >= cus) return kTile256;
+  if (per > 64 && units(128) * 4 >= cus * 3) return kMid128;
+  return kMid64;
+}
 
 template <int KIND, bool I8>
 static void launch_product(const ProdArgs &a, int R_max, hipStream_t st) {
-  if ((R_max + a.E - 1) / a.E > kTileRows) {
-    launch_tile_product(a, KIND, I8, R_max, st);
-    return;
-  }
-  // rows of an expert, were they spread evenly
+  const Form form = pick_form(a, KIND, R_max);
+  if (form == kTile256) return launch_tile_product(a, KIND, I8, R_max, st);
+  if (form != kRows) return launch_mid_product(a, KIND, I8, form == kMid64 ? 64 : 128, R_max, st);
   const int per = (R_max + a.E - 1) / a.E;
   const int mt = per <= 16 ? 1 : per <= 32 ? 2 : 4;
   int z = (per + 16 * mt - 1) / (16 * mt);
   z = z < 64 ? z : 64;
-  const dim3 grid(a.C / 16, a.E, z), block(NW * 64);
-  if (mt == 1) hipLaunchKernelGGL((k_rows_product<KIND, I8, 1>), grid, block, 0, st, a);
-  else if (mt == 2) hipLaunchKernelGGL((k_rows_product<KIND, I8, 2>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_rows_product<KIND, I8, 4>), grid, block, 0, st, a);
+  const dim3 grid(a.C / 16, a.E, z);
+  if (mt == 1) hipLaunchKernelGGL((k_rows_product<KIND, I8, 1, 8>), grid, dim3(512), 0, st, a);
+  else if (mt == 2) hipLaunchKernelGGL((k_rows_product<KIND, I8, 2, 8>), grid, dim3(512), 0, st, a);
+  else hipLaunchKernelGGL((k_rows_product<KIND, I8, 4, 8>), grid, dim3(512), 0, st, a);
 }
 
 static ProdArgs prod_args(const void *x, const int32_t *perm, int topk, const int32_t *seg, fq_shape s,

@@ -58,11 +58,12 @@ constexpr int kMaxExperts = 1024;
 // tile_start[e] = number of work units of experts 0..e-1 (e = 0..E), from
 // seg_offsets on the device: a block-wide exclusive scan in LDS. Units per
 // expert: ceil(rows / rows_per_unit), at least min_units.
+template <int THREADS = NT>
 __device__ inline void build_tile_prefix(const int32_t *seg, int E, int rows_per_unit, int min_units,
-                                  int *tile_start) {
-  __shared__ int s_wsum[NT / 64];
+                                         int *tile_start) {
+  __shared__ int s_wsum[THREADS / 64];
   int base = 0;
-  for (int e0 = 0; e0 < E; e0 += NT) {
+  for (int e0 = 0; e0 < E; e0 += THREADS) {
     const int e = e0 + threadIdx.x;
     const int nt =
         e < E ? max((seg[e + 1] - seg[e] + rows_per_unit - 1) / rows_per_unit, min_units) : 0;
@@ -77,7 +78,7 @@ __device__ inline void build_tile_prefix(const int32_t *seg, int E, int rows_per
     __syncthreads();
     int before = base, total = base;
 #pragma unroll
-    for (int k = 0; k < NT / 64; ++k) {
+    for (int k = 0; k < THREADS / 64; ++k) {
       if (k < w) before += s_wsum[k];
       total += s_wsum[k];
     }

@@ -28,9 +28,6 @@ namespace fq {
 
 namespace {
 
-typedef int i32x16 __attribute__((ext_vector_type(16)));
-typedef __attribute__((__vector_size__(16 * sizeof(int)))) int i32x16v;
-
 constexpr int BT = 256;                 // weight rows and routed rows of a tile
 constexpr int kOperand = BT * 128;      // one operand, one stage: 32 KiB
 
@@ -47,26 +44,6 @@ __device__ __forceinline__ char *stage_q() {
 // int8: the scales of the tile's weight rows (in LDS row order) and routed rows
 __shared__ __attribute__((aligned(16))) float g_scale[2 * BT];
 
-template <bool I8>
-struct Acc;
-template <>
-struct Acc<false> {
-  typedef f32x16 type;
-};
-template <>
-struct Acc<true> {
-  typedef i32x16v type;
-};
-
-template <bool I8>
-__device__ __forceinline__ void mfma32(const i32x4 &p, const i32x4 &q, typename Acc<I8>::type &acc) {
-  if constexpr (I8)
-    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(p, q, acc, 0, 0, 0);
-  else
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8v, p),
-                                                  __builtin_bit_cast(bf16x8v, q), acc, 0, 0, 0);
-}
-
 struct PTile {
   int e, c0, j0, j_end;  // expert, first output column, routed rows [j0, j_end)
 };
@@ -76,10 +53,12 @@ template <int KIND>
 constexpr int kCols = KIND == PLAIN ? 256 : 128;
 
 template <int KIND>
-__device__ __forceinline__ PTile decode(const ProdArgs &a, const int *tile_start, int n_it, int w) {
+__device__ __forceinline__ PTile decode(const ProdArgs &a, const int *tile_start, int n_it, int gm,
+                                        int w) {
   PTile t;
-  const int tile = w / n_it;
-  t.c0 = (w - tile * n_it) * kCols<KIND>;
+  int tile, it;
+  tile_of(w, n_it, gm, tile_start[a.E], tile, it);
+  t.c0 = it * kCols<KIND>;
   t.e = expert_of_tile(tile_start, a.E, tile);
   t.j0 = a.seg[t.e] + (tile - tile_start[t.e]) * BT;
   t.j_end = a.seg[t.e + 1];
@@ -93,12 +72,6 @@ __device__ __forceinline__ int weight_row(const ProdArgs &a, const PTile &t, int
   // rows 64 k .. 64 k + 63: gate (k even) or up of columns 64 (k / 2) ..
   const int up = (p >> 6) & 1, f = t.c0 + (p >> 7) * 64 + (p & 63);
   return up * a.C + min(f, a.C - 1);
-}
-
-// 16-byte chunk of a 128-byte stage row that this lane carries in the DMA
-// instructions of parity ii & 1 (the swizzle of tile.hpp over 8-row pieces)
-__device__ __forceinline__ uint32_t lane_chunk(int lane, int ii) {
-  return (uint32_t)(lane & 7) ^ (uint32_t)((4 * (ii & 1) + (lane >> 4)) & 7);
 }
 
 // The operand streams of one tile. Shares (see run_tile): waves 0-3 load all of P
@@ -247,7 +220,7 @@ __device__ __forceinline__ void store_slab32(const char *slab, uint16_t *out, si
 // 4t + 2), A the P rows and B's Q rows after the stage's last read.
 template <int KIND, bool I8, int AFMT>
 __device__ __forceinline__ int run_tile(const ProdArgs &a, ActQ aq, const int *tile_start,
-                                        int n_it, const PTile &tl, Streams<KIND> &ld, int pre,
+                                        int n_it, int gm, const PTile &tl, Streams<KIND> &ld, int pre,
                                         int next_w) {
   const int t = threadIdx.x;
   const int lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -260,7 +233,7 @@ __device__ __forceinline__ int run_tile(const ProdArgs &a, ActQ aq, const int *t
   const int wcol = tl.c0 + wi * (kCols<KIND> / 2);
   const bool live = tl.j0 + wj * 64 < tl.j_end && wcol < a.C;
 
-  typename Acc<I8>::type acc[4][2];
+  typename Acc32<I8>::type acc[4][2];
 #pragma unroll
   for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -393,7 +366,7 @@ __device__ __forceinline__ int run_tile(const ProdArgs &a, ActQ aq, const int *t
     }
   }
   if (next_w >= 0) {
-    const PTile nt = decode<KIND>(a, tile_start, n_it, next_w);
+    const PTile nt = decode<KIND>(a, tile_start, n_it, gm, next_w);
     ld.template init<I8>(a, nt, wave, lane);
     ld.template issue<0>(a, 0, wave, lane);
   }
@@ -528,7 +501,7 @@ __device__ __forceinline__ int run_tile(const ProdArgs &a, ActQ aq, const int *t
 // contiguous eighth of the tiles, dealt round-robin to its blocks, so that the tiles
 // in flight there share operand panels in its L2.
 template <int KIND, bool I8, int AFMT>
-__global__ __launch_bounds__(NT) void k_tile_product(ProdArgs a, int n_it) {
+__global__ __launch_bounds__(NT) void k_tile_product(ProdArgs a, int n_it, int gm) {
   __shared__ int tile_start[kMaxExperts + 1];
   build_tile_prefix(a.seg, a.E, BT, 0, tile_start);
   const int total = tile_start[a.E] * n_it;
@@ -540,11 +513,11 @@ __global__ __launch_bounds__(NT) void k_tile_product(ProdArgs a, int n_it) {
   int w = xcd * chunk + slot;
   if (w >= w_end) return;  // the whole block
   Streams<KIND> ld;
-  ld.template init<I8>(a, decode<KIND>(a, tile_start, n_it, w), wave, lane);
+  ld.template init<I8>(a, decode<KIND>(a, tile_start, n_it, gm, w), wave, lane);
   int pre = 0;
   for (; w < w_end; w += nslot) {
-    const PTile tl = decode<KIND>(a, tile_start, n_it, w);
-    pre = run_tile<KIND, I8, AFMT>(a, aq, tile_start, n_it, tl, ld, pre, w + nslot < w_end ? w + nslot : -1);
+    const PTile tl = decode<KIND>(a, tile_start, n_it, gm, w);
+    pre = run_tile<KIND, I8, AFMT>(a, aq, tile_start, n_it, gm, tl, ld, pre, w + nslot < w_end ? w + nslot : -1);
   }
 }
 
@@ -557,7 +530,8 @@ void launch(const ProdArgs &a, int R_max, hipStream_t st) {
   const int cus = device_cus();
   const size_t up8 = (units + 7) / 8 * 8;
   const int grid = (int)(up8 < (size_t)cus ? up8 : (size_t)cus);
-  hipLaunchKernelGGL((k_tile_product<KIND, I8, AFMT>), dim3(grid), dim3(NT), 0, st, a, n_it);
+  hipLaunchKernelGGL((k_tile_product<KIND, I8, AFMT>), dim3(grid), dim3(NT), 0, st, a, n_it,
+                     tile_group(cus / 8, n_it, ceil_div(R_max, (long)BT * a.E)));
 }
 
 template <int KIND>
