@@ -109,6 +109,32 @@ __device__ __forceinline__ uint32_t act_fq8_pair(const ActQ &q, float *x) {
   return mask;
 }
 
+// 4 elements of a per-tensor format (FP8, INT8 or none): values in place, 4 mask bits out
+__device__ __forceinline__ uint32_t act_fq4(const ActQ &q, float *x) {
+  if (q.fmt == FQ_FMT_NONE) return 0xFu;
+  uint32_t mask = 0;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    if (q.fmt == FQ_FMT_FP8_E4M3) {
+      const float z0 = x[2 * p] * q.r, z1 = x[2 * p + 1] * q.r;
+      const f32x2_t v = __builtin_amdgcn_cvt_pk_f32_fp8(
+          __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(z0), clamp448(z1), 0, false), false);
+      mask |= (uint32_t)(fabsf(z0) <= kE4M3Max) << (2 * p);
+      mask |= (uint32_t)(fabsf(z1) <= kE4M3Max) << (2 * p + 1);
+      x[2 * p] = v.x * q.s;
+      x[2 * p + 1] = v.y * q.s;
+    } else {
+#pragma unroll
+      for (int j = 2 * p; j < 2 * p + 2; ++j) {
+        const FQElem e = fq_int8(x[j], q.s, q.r);
+        x[j] = e.v;
+        mask |= (uint32_t)e.m << j;
+      }
+    }
+  }
+  return mask;
+}
+
 __device__ __forceinline__ void load16(const bf16x8_t *p, float *x) {
   bf16x8_t a = p[0], b = p[1];
   unpack8(a, x);

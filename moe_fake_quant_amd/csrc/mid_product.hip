@@ -53,15 +53,18 @@ __global__ __launch_bounds__(kThreads, NSTAGE * T > 256 ? 1 : 2) void k_mid_prod
   const ActQ q = load_actq(KIND == PLAIN || I8 ? FQ_FMT_NONE : a.afmt, a.ascale);
 
   // each XCD (block b runs on XCD b % 8) takes a contiguous eighth of the tiles
-  const int total = tile_start[a.E] * n_it;
+  // the same in every lane, which the LDS reads hide from the compiler
+  const int n_rows = __builtin_amdgcn_readfirstlane(tile_start[a.E]), total = n_rows * n_it;
   const int nslot = gridDim.x >> 3, xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
   const int chunk = (total + 7) >> 3, w_end = min((xcd + 1) * chunk, total);
   for (int w = xcd * chunk + slot; w < w_end; w += nslot) {
     int tile, it;
-    tile_of(w, n_it, gm, tile_start[a.E], tile, it);
+    tile_of(w, n_it, gm, n_rows, tile, it);
     const int c0 = it * COLS;
-    const int e = a.E == 1 ? 0 : expert_of_tile(tile_start, a.E, tile);
-    const int j0 = a.seg[e] + (tile - tile_start[e]) * T, j_end = a.seg[e + 1];
+    const int e =
+        a.E == 1 ? 0 : __builtin_amdgcn_readfirstlane(expert_of_tile(tile_start, a.E, tile));
+    const int j0 = a.seg[e] + (tile - __builtin_amdgcn_readfirstlane(tile_start[e])) * T;
+    const int j_end = a.seg[e + 1];
 
     // this lane's rows of both operands: wave w loads the rows w * T/4 .. of each
     const char *pbase = a.w + (size_t)e * a.N * a.KB;

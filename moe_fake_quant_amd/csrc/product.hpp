@@ -97,8 +97,9 @@ __device__ __forceinline__ void finish8(const ProdArgs &a, const ActQ &q, int r,
 __device__ __forceinline__ void tile_of(int w, int n_it, int gm, int n_rows, int &row, int &it) {
   const int g = w / (gm * n_it), r0 = g * gm, gs = min(gm, n_rows - r0);
   const int in = w - g * gm * n_it;
-  it = in / gs;
-  row = r0 + (in - it * gs);
+  // divisions come out of vector registers: the same in every lane, taken back
+  it = __builtin_amdgcn_readfirstlane(in / gs);
+  row = __builtin_amdgcn_readfirstlane(r0 + (in - it * gs));
 }
 // gm for `flight` tiles in flight on an XCD and about `rows` row tiles an expert: the
 // side of a square block, unless a row of tiles is too short to fill more than one

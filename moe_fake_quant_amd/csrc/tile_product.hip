@@ -57,10 +57,12 @@ __device__ __forceinline__ PTile decode(const ProdArgs &a, const int *tile_start
                                         int w) {
   PTile t;
   int tile, it;
-  tile_of(w, n_it, gm, tile_start[a.E], tile, it);
+  tile_of(w, n_it, gm, __builtin_amdgcn_readfirstlane(tile_start[a.E]), tile, it);
   t.c0 = it * kCols<KIND>;
-  t.e = expert_of_tile(tile_start, a.E, tile);
-  t.j0 = a.seg[t.e] + (tile - tile_start[t.e]) * BT;
+  // the same in every lane, which the LDS reads hide from the compiler: kept in scalar
+  // registers, as the bases and bounds formed from them are
+  t.e = __builtin_amdgcn_readfirstlane(expert_of_tile(tile_start, a.E, tile));
+  t.j0 = a.seg[t.e] + (tile - __builtin_amdgcn_readfirstlane(tile_start[t.e])) * BT;
   t.j_end = a.seg[t.e + 1];
   return t;
 }
@@ -142,9 +144,13 @@ struct Streams {
     if (wave < 4) {
       char *dst = stage_p<S>() + wave * 8192;
       if (plast >= 63) {
+        // (the step hidden from the compiler, which would keep its seven multiples)
+        uint32_t step = 8u * a.KB;
+        asm volatile("" : "+s"(step));
+        const char *p = pbase + c0;
 #pragma unroll
-        for (int ii = 0; ii < 8; ++ii)
-          dma16(pbase + (size_t)(8 * ii) * a.KB + c0, poff[ii & 1] - back[ii & 1], dst + ii * 1024);
+        for (int ii = 0; ii < 8; ++ii, p += step)
+          dma16(p, poff[ii & 1] - back[ii & 1], dst + ii * 1024);
       } else {
 #pragma unroll
         for (int ii = 0; ii < 8; ++ii) {
@@ -219,14 +225,12 @@ __device__ __forceinline__ void store_slab32(const char *slab, uint16_t *out, si
 // that phase on: B fills the Q rows that A multiplies (A has read them by phase
 // 4t + 2), A the P rows and B's Q rows after the stage's last read.
 template <int KIND, bool I8, int AFMT>
-__device__ __forceinline__ int run_tile(const ProdArgs &a, ActQ aq, const int *tile_start,
-                                        int n_it, int gm, const PTile &tl, Streams<KIND> &ld, int pre,
-                                        int next_w) {
+__device__ __forceinline__ int run_tile(const ProdArgs &a, const int *tile_start, int n_it, int gm,
+                                        const PTile &tl, Streams<KIND> &ld, int pre, int next_w) {
   const int t = threadIdx.x;
   const int lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wi = wave & 1, wj = wave >> 1;
   const bool grp_b = wave >= 4;
-  aq.fmt = AFMT;  // one instantiation a format: the epilogue's blocks then hold no branch
   const int nk = ld.nk;
   const bool cut = ld.tail < 128;
   // a wave without rows or without columns skips its reads and MFMAs
@@ -250,19 +254,24 @@ __device__ __forceinline__ int run_tile(const ProdArgs &a, ActQ aq, const int *t
     i32x4 p[4], q[2];
   };
   Frags f[2];
+  // One lane address an operand: a step's chunk 2 ks + lane / 32 differs from step 0's in
+  // bits 5 and 6 alone, so its address is an exclusive or away. Formed anew in each phase
+  // (an empty asm keeps the eight of them out of the loop's registers).
+  uint32_t pa = (uint32_t)(uintptr_t)(stage_p<0>() + nrm_off(wi * 128 + (lane & 31), lane >> 5));
+  uint32_t qa = (uint32_t)(uintptr_t)(stage_q<0>() + nrm_off(wj * 64 + (lane & 31), lane >> 5));
   auto read_half = [&](auto stage_tag, int h) {
     constexpr int S = decltype(stage_tag)::value;
+    typedef __attribute__((address_space(3))) const i32x4 lds_i32x4;
+    asm volatile("" : "+v"(pa), "+v"(qa));
 #pragma unroll
     for (int k2 = 0; k2 < 2; ++k2) {
-      const int ks = 2 * h + k2;
+      const uint32_t ks = 32u * (uint32_t)(2 * h + k2);
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        f[k2].p[s] = *reinterpret_cast<const i32x4 *>(
-            stage_p<S>() + nrm_off(wi * 128 + s * 32 + (lane & 31), 2 * ks + (lane >> 5)));
+        f[k2].p[s] = *(lds_i32x4 *)(uintptr_t)((pa ^ ks) + S * kOperand + s * 4096);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        f[k2].q[u] = *reinterpret_cast<const i32x4 *>(
-            stage_q<S>() + nrm_off(wj * 64 + u * 32 + (lane & 31), 2 * ks + (lane >> 5)));
+        f[k2].q[u] = *(lds_i32x4 *)(uintptr_t)((qa ^ ks) + S * kOperand + u * 4096);
     }
   };
   auto multiply = [&]() {
@@ -407,6 +416,9 @@ __device__ __forceinline__ int run_tile(const ProdArgs &a, ActQ aq, const int *t
     }
   } else {
     // 4 (columns) x 32 (rows) pieces (s, q) of the wave's 64 columns at f = 32 s + 8 q + 4 h
+    // one instantiation a format, so that the blocks below hold no branch; the scale is
+    // read here, where registers are free again
+    const ActQ aq = load_actq(AFMT, a.ascale);
     auto piece = [&](int u, int s, int q) -> uint2 & {
       const uint32_t row = (uint32_t)(u * 32 + jr), c = (uint32_t)(4 * s + q) ^ (row & 7u);
       return *reinterpret_cast<uint2 *>(slab + row * 128 + c * 16 + h * 8);
@@ -425,45 +437,70 @@ __device__ __forceinline__ int run_tile(const ProdArgs &a, ActQ aq, const int *t
         for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {  // a 16-block of columns: 8 here, 8 in lane ^ 32
-            float g[8], uu[8], sig[8], v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            // (the backward works in small steps: side by side they would spill, and a
+            // reload behind the output stores waits for them)
+            constexpr bool BWD = KIND == GATED_BWD;
+            auto sum = [&](int half, int k) {  // g (0) or u (1) of element k
               const int at = 8 * b + k;
               if constexpr (I8) {
                 const int p = wi * 128 + s * 32 + 16 * b + 8 * (k >> 2) + 4 * h + (k & 3);
-                g[k] = ((float)acc[s][u][at] * sx) * g_scale[p];
-                uu[k] = ((float)acc[s + 2][u][at] * sx) * g_scale[p + 64];
+                return ((float)acc[s + 2 * half][u][at] * sx) * g_scale[p + 64 * half];
               } else {
-                g[k] = acc[s][u][at];
-                uu[k] = acc[s + 2][u][at];
+                return acc[s + 2 * half][u][at];
               }
-              sig[k] = sigmoid_hw(g[k]);
-              v[k] = bf16_to_f32(f32_to_bf16((g[k] * sig[k]) * uu[k]));
-            }
-            const uint32_t m = act_fq8_pair<32>(aq, v);
-            const uint2 lo = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-            const uint2 hi = make_uint2(pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-            if constexpr (KIND == GATED) {
-              piece(u, s, 2 * b) = lo;
-              piece(u, s, 2 * b + 1) = hi;
-            } else {
+            };
+            auto grads = [&](int q, uint32_t m, const float *sig) {
               // dA's pieces lie where dG's go, lane by lane
-              uint2 &pl = piece(u, s, 2 * b), &pr = piece(u, s, 2 * b + 1);
-              const uint2 dl = pl, dr = pr;
-              const float d[8] = {lo_bf16(dl.x), hi_bf16(dl.x), lo_bf16(dl.y), hi_bf16(dl.y),
-                                  lo_bf16(dr.x), hi_bf16(dr.x), lo_bf16(dr.y), hi_bf16(dr.y)};
-              float dg[8], du[8];
+              uint2 &pc = piece(u, s, 2 * b + q);
+              const uint2 dp = pc;
+              const float d[4] = {lo_bf16(dp.x), hi_bf16(dp.x), lo_bf16(dp.y), hi_bf16(dp.y)};
+              float dg[4], du[4];
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                swiglu_grad((m >> k) & 1u ? d[k] : 0.0f, g[k], uu[k], sig[k], dg[k], du[k]);
-              pl = make_uint2(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]));
-              pr = make_uint2(pack_bf16(dg[4], dg[5]), pack_bf16(dg[6], dg[7]));
-              ku[4 * s + 2 * b] = make_uint2(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]));
-              ku[4 * s + 2 * b + 1] = make_uint2(pack_bf16(du[4], du[5]), pack_bf16(du[6], du[7]));
-              ka[4 * s + 2 * b] = lo;
-              ka[4 * s + 2 * b + 1] = hi;
-              // one block after the other: side by side they would spill
+              for (int k = 0; k < 4; ++k)
+                swiglu_grad((m >> k) & 1u ? d[k] : 0.0f, sum(0, 4 * q + k), sum(1, 4 * q + k), sig[k], dg[k],
+                            du[k]);
+              pc = make_uint2(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]));
+              ku[4 * s + 2 * b + q] = make_uint2(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]));
               __builtin_amdgcn_sched_barrier(0);
+            };
+            if constexpr (!BWD || AFMT == FQ_FMT_NVFP4) {
+              float sig[8], v[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float g = sum(0, k);
+                sig[k] = sigmoid_hw(g);
+                v[k] = bf16_to_f32(f32_to_bf16((g * sig[k]) * sum(1, k)));
+              }
+              if constexpr (BWD) __builtin_amdgcn_sched_barrier(0);
+              const uint32_t m = act_fq8_pair<32>(aq, v);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const uint2 pk = make_uint2(pack_bf16(v[4 * q], v[4 * q + 1]),
+                                            pack_bf16(v[4 * q + 2], v[4 * q + 3]));
+                if constexpr (BWD) {
+                  ka[4 * s + 2 * b + q] = pk;
+                  __builtin_amdgcn_sched_barrier(0);
+                  grads(q, m >> (4 * q), sig + 4 * q);
+                } else {
+                  piece(u, s, 2 * b + q) = pk;
+                }
+              }
+            } else {
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                float sig[4], v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float g = sum(0, 4 * q + k);
+                  sig[k] = sigmoid_hw(g);
+                  v[k] = bf16_to_f32(f32_to_bf16((g * sig[k]) * sum(1, 4 * q + k)));
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                const uint32_t m = act_fq4(aq, v);
+                ka[4 * s + 2 * b + q] = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                __builtin_amdgcn_sched_barrier(0);
+                grads(q, m, sig);
+              }
             }
           }
         const char *half = slab + u * 4096;
@@ -504,12 +541,11 @@ template <int KIND, bool I8, int AFMT>
 __global__ __launch_bounds__(NT) void k_tile_product(ProdArgs a, int n_it, int gm) {
   __shared__ int tile_start[kMaxExperts + 1];
   build_tile_prefix(a.seg, a.E, BT, 0, tile_start);
-  const int total = tile_start[a.E] * n_it;
+  const int total = __builtin_amdgcn_readfirstlane(tile_start[a.E]) * n_it;
   const int nslot = gridDim.x >> 3, xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
   const int chunk = (total + 7) >> 3;
   const int w_end = min((xcd + 1) * chunk, total);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const ActQ aq = load_actq(AFMT, a.ascale);
   int w = xcd * chunk + slot;
   if (w >= w_end) return;  // the whole block
   Streams<KIND> ld;
@@ -517,7 +553,7 @@ __global__ __launch_bounds__(NT) void k_tile_product(ProdArgs a, int n_it, int g
   int pre = 0;
   for (; w < w_end; w += nslot) {
     const PTile tl = decode<KIND>(a, tile_start, n_it, gm, w);
-    pre = run_tile<KIND, I8, AFMT>(a, aq, tile_start, n_it, gm, tl, ld, pre, w + nslot < w_end ? w + nslot : -1);
+    pre = run_tile<KIND, I8, AFMT>(a, tile_start, n_it, gm, tl, ld, pre, w + nslot < w_end ? w + nslot : -1);
   }
 }
 
