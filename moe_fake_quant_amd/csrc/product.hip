@@ -147,19 +147,22 @@ __global__ __launch_bounds__(NW * 64) void k_rows_product(ProdArgs a) {
 }  // namespace
 
 // The form of a call, by the work units that R_max rows spread evenly over the experts
-// would give. us of one call on 256 CUs, int8 / gated int8 / gated bf16, bf16 backward:
-//   rows a expert       few rows          64 x 64         128 x 128        256 x 256
+// would give. us of one call on 256 CUs, int8 / gated int8 / gated bf16, its backward:
+//   rows an expert      few rows          64 x 64             128 x 128           256 x 256
 //   one [4096 x 4096]
-//     16               8 / 9 / 14, 15   12 / 12 / 19, 19  23 / 24 / 43, 44  37 / 48 / 67, 89
-//     64              13 / 16 / 26, 27  12 / 12 / 20, 21  21 / 20 / 30, 32  37 / 48 / 68, 91
-//     512             87 / 55 / 94, 97  19 / 18 / 30, 33  25 / 23 / 32, 37  45 / 60 / 84, 110
-//     1024                              33 / 32 / 58, 61  29 / 27 / 40, 43  46 / 60 / 84, 111
-//     2048                              64 / 61 / 110, 117  51 / 43 / 69, 73  49 / 61 / 85, 113
-//     4096                              126 / 121 / 236, 258  92 / 83 / 138, 149  64 / 69 / 112, 133
+//     16                8 / 9 / 14, 15    12 / 12 / 19, 19    17 / 18 / 29, 29    36 / 37 / 66, 68
+//     64                13 / 16 / 26, 27  12 / 12 / 20, 21    20 / 19 / 30, 32    36 / 37 / 66, 70
+//     512               87 / 55 / 94, 97  18 / 17 / 29, 32    25 / 21 / 32, 37    44 / 46 / 81, 86
+//     1024                                31 / 31 / 56, 58    28 / 24 / 39, 41    44 / 46 / 82, 86
+//     2048                                59 / 57 / 107, 114  51 / 42 / 68, 72    47 / 47 / 81, 86
 //   128 of [1536 x 2048]
-//     16            121 / 131 / 211, 227  87 / 82 / 147, 155  92 / 88 / 154, 159  91 / 111 / 165, 205
-//     128                               154 / 146 / 249, 260  143 / 114 / 202, 233  105 / 120 / 175, 233
-//     256                               264 / 252 / 421, 445  229 / 185 / 275, 308  132 / 141 / 216, 291
+//     16            121 / 131 / 211, 227  85 / 82 / 146, 155  92 / 88 / 155, 158  90 / 90 / 162, 170
+//     64                                  101 / 95 / 186, 193 114 / 97 / 198, 211 93 / 92 / 202, 214
+//     128                                 152 / 143 / 249, 259  142 / 114 / 201, 233  104 / 98 / 200, 217
+//     256                                 263 / 252 / 416, 443  227 / 184 / 273, 306  132 / 126 / 215, 237
+//   16 of [1536 x 2048]
+//     16                                  15 / 15 / 28, 28    17 / 17 / 29, 29    26 / 27 / 46, 49
+//     1024                                116 / 107 / 176, 190  101 / 78 / 110, 132  66 / 64 / 103, 113
 enum Form { kRows, kMid64, kMid128, kTile256 };
 
 static Form pick_form(const ProdArgs &a, int kind, int R_max) {

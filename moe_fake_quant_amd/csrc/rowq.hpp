@@ -7,12 +7,15 @@
 namespace fq {
 
 // A row of nv 8-element vectors lies over WPR waves: lane `lane` of the row's
-// WPR * 64 lanes holds the vectors lane + i * WPR * 64. Blocks are 256 threads:
-// four rows (WPR = 1, no barrier) or one (WPR = 4).
-constexpr int kRowThreads = 256;
+// WPR * 64 lanes holds the vectors lane + i * WPR * 64. A block is four rows of one
+// wave each (no barrier), or one row.
+template <int WPR>
+constexpr int kRowThreads = WPR == 1 ? 256 : WPR * 64;
+template <int WPR>
+constexpr int kBlockRows = WPR == 1 ? 4 : 1;
 
 // Sums of N values over the row's lanes, the same in each of them and in a fixed
-// order. WPR = 4: every thread of the block takes part; `red` has room for 4 * N
+// order. WPR > 1: every thread of the block takes part; `red` has room for WPR * N
 // floats and is free again at the next barrier.
 template <int WPR, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float *red) {
