@@ -467,3 +467,4 @@ def fq_norm_residual_bwd(dy, dn, y, b, gate, alpha, w_post, w_pre, eps, T, H, dx
 
 
 from .layer import MoEFakeQuantLayer  # noqa: E402,F401
+from .block import MoEFakeQuantBlock  # noqa: E402,F401

@@ -33,8 +33,16 @@ scales, 2F + H/topk bytes a routed row (and 0.8 to 25 % for the scales) instead 
 buffer is free in between, and ``scratch_of`` lets the layers of a model share
 one set of them.
 
+With ``recompute`` the forward keeps nothing of the routed rows: gate_up, SwiGLU
+and the activation FQ are one kernel (fq_grouped_gated_fwd, h never written), and the
+backward forms h again from the layer input, at the price of that GEMM. Its g and u
+are not rounded to bf16 in between, so results differ from the other modes' in that
+rounding.
+
 After training, ``export()`` gives the stored form of both stacks and
-``forward_tokens`` runs up to 128 tokens on it, as a decoding loop does.
+``forward_tokens`` runs up to 128 tokens on it, as a decoding loop does;
+``forward_int8`` runs any number of tokens on int8 stacks (w8a8), activations
+quantized with a scale for each token as they come.
 """
 from __future__ import annotations
 
@@ -43,17 +51,19 @@ from typing import Optional, Tuple
 import torch
 
 from . import (ActQ, FMT_FP8_E4M3, FMT_INT4, FMT_INT8, FMT_NONE, FMT_NVFP4, FQ_GROUP_TENSOR,
-               FQ_OP_ACT_SCALE_GRAD, FQ_OP_GEMM_BWD, FQ_OP_GEMM_FWD, FQ_OP_MOE_TOKENS,
-               FQ_OP_PERMUTE, StoredW, WeightQ, fq_actfq, fq_ckpt_load, fq_ckpt_save,
-               fq_export_scales, fq_grouped_gemm_bwd_scale, fq_grouped_gemm_fwd,
-               fq_grouped_gemm_fwd_tokens, fq_grouped_gemm_wgrad_tokens, fq_moe_combine,
-               fq_moe_combine_bwd, fq_moe_permute, fq_moe_tokens, fq_moe_unpermute_reduce,
-               fq_quantize_stacked, fq_swiglu_actfq, fq_swiglu_actfq_ckpt, fq_swiglu_bwd,
-               fq_swiglu_bwd_ckpt, fq_workspace_bytes, observer_absmax_init)
+               FQ_OP_ACT_SCALE_GRAD, FQ_OP_GATED, FQ_OP_GEMM_BWD, FQ_OP_GEMM_FWD, FQ_OP_GEMM_INT8,
+               FQ_OP_MOE_TOKENS, FQ_OP_PERMUTE, StoredW, WeightQ, fq_actfq, fq_ckpt_load,
+               fq_ckpt_save, fq_export_scales, fq_grouped_gated_bwd, fq_grouped_gated_fwd,
+               fq_grouped_gated_int8, fq_grouped_gemm_bwd_scale, fq_grouped_gemm_fwd,
+               fq_grouped_gemm_fwd_tokens, fq_grouped_gemm_int8, fq_grouped_gemm_wgrad_tokens,
+               fq_moe_combine, fq_moe_combine_bwd, fq_moe_permute, fq_moe_tokens,
+               fq_moe_unpermute_reduce, fq_quantize_stacked, fq_quantize_tokens, fq_swiglu_actfq,
+               fq_swiglu_actfq_ckpt, fq_swiglu_bwd, fq_swiglu_bwd_ckpt, fq_workspace_bytes,
+               observer_absmax_init)
 
 MAX_TOKENS = 128   # of forward_tokens (fq_moe_tokens)
 
-# buffers that hold nothing from a checkpointed layer's forward to its backward
+# buffers that hold nothing from a checkpointed or recomputing layer's forward to its backward
 _SCRATCH = ("xq_tok", "x_back", "a", "aq", "o", "out", "do", "daq", "dh", "dxq", "dx", "ws", "ws2",
             "side", "ev_do", "ev_dh")
 
@@ -72,16 +82,18 @@ class MoEFakeQuantLayer:
     def __init__(self, w_gu: torch.Tensor, w_d: torch.Tensor, wfmt: int, afmt: int, T_max: int,
                  topk: int, expert_begin: int = 0, group: Optional[int] = None,
                  learn_act_scales: bool = False, ckpt: Optional[Tuple[int, int]] = None,
-                 scratch_of: Optional["MoEFakeQuantLayer"] = None):
+                 scratch_of: Optional["MoEFakeQuantLayer"] = None, recompute: bool = False):
         """w_gu [E, 2F, H], w_d [E, H, F] bf16 on the device (frozen). group None =
         one scale per output channel (group = K of each stack); FQ_GROUP_TENSOR =
         one scale per expert matrix (int8 / fp8). learn_act_scales:
         the backward also produces the activation-scale gradients (FP8 / INT8).
         ckpt (fmt, group): FMT_INT8 or FMT_FP8_E4M3 checkpoints of h and the
         input (group as in fq_ckpt_save, dividing F and H). scratch_of: another
-        checkpointed layer of the same sizes and formats, on the same stream,
-        whose buffers this one shares: out and dx hold the last layer's, so that
-        a layer whose input was another's out takes None in its backward."""
+        checkpointed (or recomputing) layer of the same sizes and formats, on the
+        same stream, whose buffers this one shares: out and dx hold the last layer's, so
+        that a layer whose input was another's out takes None in its backward (a
+        recomputing one a copy of its input). recompute: h is formed again in the
+        backward; not with ckpt or learn_act_scales."""
         assert w_gu.dtype == torch.bfloat16 and w_d.dtype == torch.bfloat16
         self.dev = w_gu.device
         self.E, F2, self.H = w_gu.shape
@@ -104,11 +116,16 @@ class MoEFakeQuantLayer:
                     or self.F % cg or self.H % cg:
                 raise ValueError("ckpt is (FMT_INT8 or FMT_FP8_E4M3, a power of two from 16 to 512 "
                                  f"that divides F={self.F} and H={self.H}), not {ckpt}")
-        self.ckpt = ckpt
+        if recompute and (ckpt is not None or learn_act_scales):
+            raise ValueError("recompute excludes ckpt and learn_act_scales (a scale's gradient is "
+                             "formed from a kept or checkpointed h)")
+        self.ckpt, self.recompute = ckpt, recompute
+        self._holds_h = ckpt is None and not recompute
         if scratch_of is not None:
             o = scratch_of
-            if ckpt is None or o.ckpt is None:
-                raise ValueError("only checkpointed layers can share their buffers")
+            if (ckpt is None, recompute) != (o.ckpt is None, o.recompute) or self._holds_h:
+                raise ValueError("only checkpointed layers, or recomputing ones, can share their "
+                                 "buffers")
             if (o.dev, o.E, o.H, o.F, o.T_max, o.topk) != (self.dev, self.E, self.H, self.F, T_max,
                                                            topk):
                 raise ValueError("layers that share buffers must have the same sizes and device")
@@ -149,7 +166,7 @@ class MoEFakeQuantLayer:
             self.dh = torch.empty(R, 2 * F, **bf)
             # a checkpointed h is read once, by the pass that saves it, and dh
             # is first written after that
-            self.h = torch.empty(R, 2 * F, **bf) if ckpt is None else self.dh
+            self.h = torch.empty(R, 2 * F, **bf) if self._holds_h else self.dh
             self.x_back = None if ckpt is None else torch.empty(T_max, H, **bf)
             self.dxq = torch.empty(R, H, **bf)
             self.dx = torch.empty(T_max, H, **bf)
@@ -169,7 +186,8 @@ class MoEFakeQuantLayer:
                      fq_workspace_bytes(FQ_OP_GEMM_FWD, self.shape_gu, R, 0),
                      fq_workspace_bytes(FQ_OP_GEMM_FWD, self.shape_d, R, 0),
                      fq_workspace_bytes(FQ_OP_GEMM_BWD, self.shape_gu, R, 0),
-                     fq_workspace_bytes(FQ_OP_GEMM_BWD, self.shape_d, R, 0), 256)
+                     fq_workspace_bytes(FQ_OP_GEMM_BWD, self.shape_d, R, 0),
+                     fq_workspace_bytes(FQ_OP_GATED, self.shape_gu, R, 0), 256)
             self.ws = torch.empty(ws, dtype=torch.uint8, device=self.dev)
             self.ws2 = torch.empty(ws, dtype=torch.uint8, device=self.dev)
             self.side = torch.cuda.Stream(device=self.dev)   # default priority
@@ -213,26 +231,37 @@ class MoEFakeQuantLayer:
             observer_absmax_init(self.a[:R], (1, R, self.F), self.afmt, 16, 1, self.aq2.scale)
 
     # ---------------------------------------------------------- hot path --
-    def _gate_up_fwd(self, x: torch.Tensor, T: int):
-        """FQ_a of each token row once (the rows themselves without an
-        activation format), then the gate_up GEMM over the routed rows."""
+    def _token_input(self, x: torch.Tensor, T: int):
+        """FQ_a of each token row once (the rows themselves without an activation
+        format): the gate_up operand."""
         if self.afmt == FMT_NONE:
             self._x_tok = x
         else:
             fq_actfq(x, T, self.H, self.aq1, self.xq_tok)
             self._x_tok = self.xq_tok
+
+    def _gate_up_fwd(self, x: torch.Tensor, T: int):
+        """The gate_up GEMM over the routed rows of the fake-quantized tokens."""
+        self._token_input(x, T)
         fq_grouped_gemm_fwd_tokens(self._x_tok, T, self.perm, self.topk, self.R_max, self.seg,
                                    self.shape_gu, None, self.wfq_gu, self.q_gu, self.h, self.ws)
 
     def forward(self, x: torch.Tensor, expert_ids: torch.Tensor, probs: torch.Tensor,
                 keep_a: bool = False) -> torch.Tensor:
         T = x.shape[0]
+        if keep_a and self.recompute:
+            raise ValueError("a recomputing layer does not form A before its fake-quant")
         self.route(expert_ids)
-        self._gate_up_fwd(x, T)
-        if self.ckpt is None:
+        if self.recompute:
+            self._token_input(x, T)
+            fq_grouped_gated_fwd(self._x_tok, T, self.perm, self.topk, self.R_max, self.seg,
+                                 self.shape_gu, self.wfq_gu, self.aq2, self.aq, self.ws)
+        elif self.ckpt is None:
+            self._gate_up_fwd(x, T)
             fq_swiglu_actfq(self.h, self.R_max, self.n_rows, self.F, self.aq2,
                             self.a if keep_a else None, self.aq)
         else:
+            self._gate_up_fwd(x, T)
             fq_ckpt_save(x, T, self.H, None, *self.ckpt, self.x_codes[:T], self.x_scale[:T])
             fq_swiglu_actfq_ckpt(self.h, self.R_max, self.n_rows, self.F, self.aq2, *self.ckpt,
                                  self.a if keep_a else None, self.aq, self.h_codes, self.h_scale)
@@ -281,11 +310,7 @@ class MoEFakeQuantLayer:
         if x is None:
             x = self.x_back[:T]
             fq_ckpt_load(self.x_codes[:T], self.x_scale[:T], T, self.H, None, *self.ckpt, x)
-        if self.afmt == FMT_NONE:
-            self._x_tok = x
-        else:
-            fq_actfq(x, T, self.H, self.aq1, self.xq_tok)
-            self._x_tok = self.xq_tok
+        self._token_input(x, T)
         return x
 
     def backward(self, x: Optional[torch.Tensor], probs: torch.Tensor, dout: torch.Tensor):
@@ -295,10 +320,10 @@ class MoEFakeQuantLayer:
         T = self.T if x is None else x.shape[0]
         if x is None and self.ckpt is None:
             raise ValueError("backward without x needs a checkpointed layer")
-        if self.ckpt is not None and x is not None \
+        if not self._holds_h and x is not None \
                 and x.untyped_storage().data_ptr() in self._scratch_at:
-            raise ValueError("x lies in a buffer of the checkpointed layers that has been overwritten "
-                             "since the forward: pass None (the input's checkpoint), or a copy")
+            raise ValueError("x lies in a buffer of the layers that has been overwritten since the "
+                             "forward: pass a copy, or None for the input's checkpoint")
         main = torch.cuda.current_stream(self.dev)
         if self.overlap_wgrad:
             # the side stream's previous step (and anything else the caller
@@ -313,16 +338,23 @@ class MoEFakeQuantLayer:
         down_wgrad = lambda ws: fq_grouped_gemm_bwd_scale(  # noqa: E731
             self.do, self.aq, self.R_max, self.seg, self.shape_d, self.w_d, self.wfq_d, self.q_d,
             None, None, self.ds_d, self.dzp_d, ws)
-        if self.ckpt is None:
+        if self._holds_h:
             self._wgrad(self.ev_do, down_wgrad)
             fq_swiglu_bwd(self.daq, self.h, self.R_max, self.n_rows, self.F, self.aq2, self.dh,
                           self.ds_a2, self.ws)
             self.ev_dh.record(main)
         else:
             # FQ_a(A) comes out of the SwiGLU backward, so this wgrad starts behind it
-            fq_swiglu_bwd_ckpt(self.daq, self.h_codes, self.h_scale, self.R_max, self.n_rows,
-                               self.F, *self.ckpt, self.aq2, self.dh, self.aq, self.ds_a2, self.ws)
-            x = self._restore_input(x, T)
+            if self.recompute:
+                self._token_input(x, T)
+                fq_grouped_gated_bwd(self.daq, self._x_tok, T, self.perm, self.topk, self.R_max,
+                                     self.seg, self.shape_gu, self.wfq_gu, self.aq2, self.dh,
+                                     self.aq, self.ws)
+            else:
+                fq_swiglu_bwd_ckpt(self.daq, self.h_codes, self.h_scale, self.R_max, self.n_rows,
+                                   self.F, *self.ckpt, self.aq2, self.dh, self.aq, self.ds_a2,
+                                   self.ws)
+                x = self._restore_input(x, T)
             self.ev_dh.record(main)
             self._wgrad(self.ev_dh, down_wgrad)
         fq_grouped_gemm_bwd_scale(self.dh, None, self.R_max, self.seg, self.shape_gu, self.w_gu,
@@ -401,3 +433,69 @@ class MoEFakeQuantLayer:
         fq_moe_tokens(x, T, self.H, self.F, expert_ids, probs, self.topk, self.expert_begin,
                       self.E, *self.stored, self.aq1, self.aq2, out, self.tok_ws)
         return out
+
+    def _int8_buffers(self):
+        R, bf = self.R_max, dict(dtype=torch.bfloat16, device=self.dev)
+        i32 = dict(dtype=torch.int32, device=self.dev)
+        u8, f32 = dict(dtype=torch.uint8, device=self.dev), dict(dtype=torch.float32, device=self.dev)
+        n = max(fq_workspace_bytes(FQ_OP_PERMUTE, (self.E, 0, 0), R, 0),
+                fq_workspace_bytes(FQ_OP_GATED, self.shape_gu, R, 0),
+                fq_workspace_bytes(FQ_OP_GEMM_INT8, self.shape_d, R, 0), 256)
+        self.i8 = dict(x_codes=torch.empty(self.T_max, self.H, **u8), x_scale=torch.empty(self.T_max, **f32),
+                       perm=torch.empty(R, **i32), row_of=torch.empty(self.T_max, self.topk, **i32),
+                       seg=torch.empty(self.E + 1, **i32), a=torch.empty(R, self.F, **bf),
+                       a_codes=torch.empty(R, self.F, **u8), a_scale=torch.empty(R, **f32),
+                       o=torch.empty(R, self.H, **bf), out=torch.empty(self.T_max, self.H, **bf),
+                       ws=torch.empty(n, **u8))
+
+    def _check_routed(self, T, expert_ids, probs):
+        if T > self.T_max:
+            raise ValueError(f"{T} tokens, but the layer has room for {self.T_max}")
+        for name, t, dt in (("expert_ids", expert_ids, torch.int32), ("probs", probs, torch.float32)):
+            if t.shape != (T, self.topk) or t.dtype != dt:
+                raise ValueError(f"{name} must be {dt} [{T}, {self.topk}]")
+
+    def _check_int8(self):
+        if getattr(self, "stored", None) is None:
+            raise ValueError("forward_int8 needs export() first")
+        for st, K in zip(self.stored, (self.H, self.F)):
+            if st.fmt != FMT_INT8 or st.group not in (K, FQ_GROUP_TENSOR):
+                raise ValueError("forward_int8 needs int8 stacks with a scale for each channel or matrix")
+        if not hasattr(self, "i8"):
+            self._int8_buffers()
+
+    def forward_int8(self, x: torch.Tensor, expert_ids: torch.Tensor,
+                     probs: torch.Tensor) -> torch.Tensor:
+        """The layer over the exported int8 stacks for up to T_max tokens: the tokens and
+        the SwiGLU rows as int8 codes with a scale each, both products on the codes. The
+        result is the layer's own buffer, overwritten by the next call; nothing that a
+        backward needs is touched."""
+        self._check_int8()
+        T = x.shape[0]
+        if x.shape != (T, self.H) or x.dtype != torch.bfloat16:
+            raise ValueError(f"x must be bf16 [T, {self.H}]")
+        self._check_routed(T, expert_ids, probs)
+        b = self.i8
+        fq_quantize_tokens(x, T, self.H, None, b["x_codes"], b["x_scale"])
+        return self.forward_int8_codes(b["x_codes"], b["x_scale"], T, expert_ids, probs)
+
+    def forward_int8_codes(self, x_codes: torch.Tensor, x_scale: torch.Tensor, T: int,
+                           expert_ids: torch.Tensor, probs: torch.Tensor) -> torch.Tensor:
+        """forward_int8 from codes that are there already (a norm's): x_codes uint8
+        [>= T, H], x_scale fp32 [>= T]."""
+        self._check_int8()
+        self._check_routed(T, expert_ids, probs)
+        if x_codes.dtype != torch.uint8 or x_codes.dim() != 2 or x_codes.shape[1] != self.H \
+                or x_codes.shape[0] < T or x_scale.dtype != torch.float32 or x_scale.numel() < T:
+            raise ValueError(f"x_codes must be uint8 [>= {T}, {self.H}], x_scale float32 [>= {T}]")
+        b, w_gu, w_d = self.i8, *self.stored
+        R = T * self.topk
+        fq_moe_permute(expert_ids, T, self.topk, self.expert_begin, self.E, b["perm"], b["row_of"][:T],
+                       b["seg"], b["ws"])
+        fq_grouped_gated_int8(x_codes, x_scale, T, b["perm"], self.topk, R, b["seg"], self.shape_gu, w_gu,
+                              b["a"], b["ws"])
+        fq_quantize_tokens(b["a"], R, self.F, b["seg"][self.E:], b["a_codes"], b["a_scale"])
+        fq_grouped_gemm_int8(b["a_codes"], b["a_scale"], R, None, 1, R, b["seg"], self.shape_d, w_d, b["o"],
+                             b["ws"])
+        fq_moe_combine(b["o"], probs, b["row_of"][:T], T, self.topk, self.H, b["out"][:T])
+        return b["out"][:T]

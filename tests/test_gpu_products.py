@@ -58,7 +58,10 @@ def test_token_codes_bitexact(rows, K):
 INT8 = [(1, 1, 1, 16, 16, 0, False), (1, 1, 1, 512, 4096, 0, False), (1, 16, 1, 272, 80, 0, False),
         (1, 17, 1, 48, 1040, 3, False), (4, 9, 3, 64, 48, 2, False), (5, 50, 2, 96, 272, 7, True),
         (3, 300, 1, 1040, 368, 11, True), (2, 257, 2, 512, 128, 0, False), (1, 600, 1, 256, 640, 1, False),
-        (7, 150, 4, 304, 400, 40, True), (130, 40, 2, 32, 64, 5, False), (1, 33, 1, 4096, 144, 0, False)]
+        (7, 150, 4, 304, 400, 40, True), (130, 40, 2, 32, 64, 5, False), (1, 33, 1, 4096, 144, 0, False),
+        # enough tiles of 256, and of 128 (more than CUs, and fewer), to be taken
+        (64, 1300, 4, 1056, 144, 60, True), (64, 1300, 4, 1056, 656, 0, False),
+        (16, 700, 3, 1056, 272, 9, True), (8, 800, 3, 1056, 400, 5, False)]
 
 
 @pytest.mark.parametrize("E,T,topk,N,K,spare,skew", INT8)
@@ -139,7 +142,10 @@ def test_int8_a_row_that_is_not_finite_is_nan_and_alone():
 GATED = [(1, 1, 1, 16, 16, 0, False), (1, 1, 1, 2048, 256, 0, False), (1, 16, 1, 80, 48, 0, False),
          (1, 19, 1, 272, 144, 2, False), (4, 9, 3, 48, 32, 2, False), (5, 50, 2, 208, 80, 7, True),
          (2, 257, 2, 64, 256, 0, False), (3, 300, 1, 368, 528, 11, True), (1, 600, 1, 128, 128, 1, False),
-         (7, 150, 4, 336, 112, 40, True), (130, 40, 2, 32, 16, 5, False), (1, 130, 1, 1040, 768, 0, False)]
+         (7, 150, 4, 336, 112, 40, True), (130, 40, 2, 32, 16, 5, False), (1, 130, 1, 1040, 768, 0, False),
+         # enough tiles of 256, and of 128 (more than CUs, and fewer), to be taken
+         (64, 1300, 4, 144, 528, 60, True), (64, 1300, 4, 272, 640, 0, False),
+         (16, 700, 3, 272, 528, 9, True), (8, 800, 3, 208, 528, 5, False)]
 ACTS = [(O.FMT_NONE, 1.0), (O.FMT_FP8, 0.02), (O.FMT_INT8, 0.05), (O.FMT_NVFP4, 0.01)]
 
 
@@ -239,7 +245,8 @@ def test_gated_forward_on_normal_inputs(E, T, topk, H, Fc):
     _check_fq(host_bits(aq), lo, hi, O.FMT_NONE, 1.0, T * topk, Fc)
 
 
-@pytest.mark.parametrize("T,H,Fc", [(5, 48, 32), (300, 80, 144), (600, 336, 400)])
+@pytest.mark.parametrize("T,H,Fc", [(5, 48, 32), (300, 80, 144), (600, 336, 400), (2500, 144, 1040),
+                                    (9000, 144, 2064)])
 def test_gated_nan_stays_in_its_row_and_column(T, H, Fc):
     """A NaN in a token, in the token behind the last row's, and in one weight row of
     each expert: the ends of rows inside a tile bring nothing of the neighbours in."""
@@ -302,7 +309,7 @@ def test_no_rows_write_nothing():
     assert torch.all(y == FILL) and torch.all(a == FILL) and torch.all(sx == 1.0)
 
 
-@pytest.mark.parametrize("T,H,Fc", [(3, 512, 64), (700, 256, 272)])
+@pytest.mark.parametrize("T,H,Fc", [(3, 512, 64), (700, 256, 272), (1500, 256, 1040), (9000, 208, 1040)])
 def test_repeats_streams_and_replays_are_bitwise_equal(T, H, Fc):
     """The w8a8 chain and the gated block with its backward: again, on another
     stream with a workspace of its own, and from a captured graph over new inputs."""
