@@ -38,6 +38,8 @@ __global__ __launch_bounds__(kThreads, NSTAGE * T > 256 ? 1 : 2) void k_mid_prod
   static_assert(NSTAGE * 2 * kOp >= T * T * 4, "the sums go through the ring");
   __shared__ __attribute__((aligned(1024))) char ring[NSTAGE * 2 * kOp];
   __shared__ int tile_start[kMaxExperts + 1];
+  // int8: the scales of the tile's weight rows and routed rows
+  __shared__ __attribute__((aligned(16))) float scales[I8 ? 2 * T : 4];
   if (a.E == 1) {
     if (threadIdx.x == 0) {
       tile_start[0] = 0;
@@ -78,6 +80,12 @@ __global__ __launch_bounds__(kThreads, NSTAGE * T > 256 ? 1 : 2) void k_mid_prod
       const int j = min(j0 + r, j_end - 1);
       const uint32_t row = a.perm ? a.topk.div((uint32_t)a.perm[j]) : (uint32_t)(j - j0);
       qoff[ii] = row * a.KB + ch;
+    }
+    // on its way during the contraction, put into `scales` behind it
+    float scale = 0.0f;
+    if constexpr (I8) {
+      if (t < T) scale = a.sw[a.sw_rows ? (size_t)e * a.N + weight_row<KIND, T>(a, c0, t) : (size_t)e];
+      else if (t < 2 * T) scale = a.sx[x_row(a, min(j0 + t - T, j_end - 1))];
     }
     // lanes past the contraction's end read their stage's first chunk, cleared below
     uint32_t back[2];
@@ -200,6 +208,7 @@ __global__ __launch_bounds__(kThreads, NSTAGE * T > 256 ? 1 : 2) void k_mid_prod
     // c ^ (j % (T / 4)): a wave's writes (32 rows, one chunk) spread over the banks
     __syncthreads();
     int *sum = reinterpret_cast<int *>(ring);
+    if (I8 && t < 2 * T) scales[t] = scale;
     auto at = [&](int j, int p) { return sum + j * T + (((p >> 2) ^ (j & (T / 4 - 1))) << 2); };
 #pragma unroll
     for (int s = 0; s < NM; ++s)
@@ -222,19 +231,19 @@ __global__ __launch_bounds__(kThreads, NSTAGE * T > 256 ? 1 : 2) void k_mid_prod
     for (int i = t; i < T * CH; i += kThreads) {
       const int j = i / CH, cc = (i % CH) * 8, r = j0 + j;
       const bool live = r < j_end && c0 + cc < a.C;
-      int g8[8], u8[8];
       // the piece's place among the tile's weight rows
       const int p = KIND == PLAIN ? cc : (cc / (T / 4)) * (T / 2) + cc % (T / 4);
-      *reinterpret_cast<i32x4 *>(g8) = *reinterpret_cast<const i32x4 *>(at(j, p));
-      *reinterpret_cast<i32x4 *>(g8 + 4) = *reinterpret_cast<const i32x4 *>(at(j, p + 4));
-      if constexpr (KIND != PLAIN) {
-        *reinterpret_cast<i32x4 *>(u8) = *reinterpret_cast<const i32x4 *>(at(j, p + T / 4));
-        *reinterpret_cast<i32x4 *>(u8 + 4) = *reinterpret_cast<const i32x4 *>(at(j, p + T / 4 + 4));
-      }
+      auto sums = [&](int p, float *v) {
+        int w[8];
+        *reinterpret_cast<i32x4 *>(w) = *reinterpret_cast<const i32x4 *>(at(j, p));
+        *reinterpret_cast<i32x4 *>(w + 4) = *reinterpret_cast<const i32x4 *>(at(j, p + 4));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          v[k] = I8 ? ((float)w[k] * scales[T + j]) * scales[p + k] : __int_as_float(w[k]);
+      };
       float g[8], u[8];
-      const int rr = min(r, j_end - 1), cl = min(c0 + cc, a.C - 8);
-      sums8<I8>(a, e, rr, cl, g8, g);
-      if constexpr (KIND != PLAIN) sums8<I8>(a, e, rr, a.C + cl, u8, u);
+      sums(p, g);
+      if constexpr (KIND != PLAIN) sums(p + T / 4, u);
       finish8<KIND>(a, q, r, c0 + cc, g, u, live);
     }
     __syncthreads();  // the sums are read before the next tile's stages land

@@ -150,19 +150,17 @@ __global__ __launch_bounds__(NW * 64) void k_rows_product(ProdArgs a) {
 // would give. us of one call on 256 CUs, int8 / gated int8 / gated bf16, its backward:
 //   rows an expert      few rows          64 x 64             128 x 128           256 x 256
 //   one [4096 x 4096]
-//     16                8 / 9 / 14, 15    12 / 12 / 19, 19    17 / 18 / 29, 29    36 / 37 / 66, 68
-//     64                13 / 16 / 26, 27  12 / 12 / 20, 21    20 / 19 / 30, 32    36 / 37 / 66, 70
-//     512               87 / 55 / 94, 97  18 / 17 / 29, 32    25 / 21 / 32, 37    44 / 46 / 81, 86
-//     1024                                31 / 31 / 56, 58    28 / 24 / 39, 41    44 / 46 / 82, 86
-//     2048                                59 / 57 / 107, 114  51 / 42 / 68, 72    47 / 47 / 81, 86
+//     16                8 / 9 / 14, 15    11 / 11 / 19, 19    16 / 16 / 29, 29    36 / 37 / 66, 68
+//     64                13 / 16 / 26, 27  11 / 12 / 20, 21    17 / 17 / 30, 32    36 / 37 / 66, 70
+//     512               87 / 55 / 94, 97  17 / 17 / 30, 31    19 / 19 / 33, 36    44 / 46 / 81, 86
+//     1024                                29 / 29 / 55, 57    22 / 21 / 37, 40    44 / 46 / 82, 86
+//     2048                                55 / 54 / 107, 117  37 / 36 / 66, 72    50 / 49 / 83, 86
 //   128 of [1536 x 2048]
-//     16            121 / 131 / 211, 227  85 / 82 / 146, 155  92 / 88 / 155, 158  90 / 90 / 162, 170
-//     64                                  101 / 95 / 186, 193 114 / 97 / 198, 211 93 / 92 / 202, 214
-//     128                                 152 / 143 / 249, 259  142 / 114 / 201, 233  104 / 98 / 200, 217
-//     256                                 263 / 252 / 416, 443  227 / 184 / 273, 306  132 / 126 / 215, 237
-//   16 of [1536 x 2048]
-//     16                                  15 / 15 / 28, 28    17 / 17 / 29, 29    26 / 27 / 46, 49
-//     1024                                116 / 107 / 176, 190  101 / 78 / 110, 132  66 / 64 / 103, 113
+//     16            121 / 131 / 211, 227  80 / 79 / 146, 155  86 / 83 / 155, 158  90 / 90 / 162, 170
+//     64                                  95 / 92 / 167, 178  94 / 89 / 164, 180  93 / 92 / 202, 214
+//     128                                 143 / 140 / 249, 259  120 / 111 / 201, 233  104 / 98 / 200, 217
+//     256                                 250 / 245 / 416, 443  190 / 175 / 273, 306  132 / 126 / 215, 237
+//   64 of [2048 x 768], 1024 rows         298 / 279 / 411, 503  211 / 179 / 281, 366  154 / 143 / 216, 270
 enum Form { kRows, kMid64, kMid128, kTile256 };
 
 static Form pick_form(const ProdArgs &a, int kind, int R_max) {
