@@ -584,9 +584,10 @@ fq_status fq_swiglu_bwd_ckpt(const uint16_t *daq_bf16, const uint8_t *codes, con
  *   (scale [E, N]) or FQ_GROUP_TENSOR (scale [E]); the other fields unused.
  *   Rows from seg_offsets[E] on are left untouched.
  * K and N (gated: F) multiples of 16, K <= 131071, E <= 1024; an expert's codes,
- * and with perm the token rows, below 4 GiB. codes, x_codes, y and a 16-byte
- * aligned, scales 4-byte. Workspace: fq_workspace_bytes(FQ_OP_GEMM_INT8, shape,
- * R_max, 0), for the gated product FQ_OP_GATED.
+ * and with perm the token rows, below 4 GiB; rows * K < 2^35 for the codes. codes,
+ * x_codes, y and a 16-byte aligned, scales 4-byte. Outputs must not overlap inputs.
+ * Workspace: fq_workspace_bytes(FQ_OP_GEMM_INT8, shape, R_max, 0), for the gated
+ * product FQ_OP_GATED (0 bytes: ws may be NULL).
  * ---------------------------------------------------------------------- */
 fq_status fq_quantize_tokens(const uint16_t *x_bf16, int32_t rows, int32_t K, const int32_t *n_rows,
                              uint8_t *codes, float *scale, fq_stream stream);
@@ -614,9 +615,12 @@ fq_status fq_grouped_gated_int8(const uint8_t *x_codes, const float *x_scale, in
  * shape {E, 2F, H}; w_fq [E, 2F, H] bf16, used as given (fq_quantize_stacked's
  * output, or the raw weights). x_bf16 [x_rows, H] already fake-quantized, read
  * through perm / topk or (perm NULL) by routed row, as for the int8 products.
- * Rows from seg_offsets[E] on are left untouched. H, F % 16 == 0, E <= 1024; an
- * expert's matrix, and with perm the token rows, below 4 GiB.
- * Workspace: fq_workspace_bytes(FQ_OP_GATED, shape, R_max, 0).
+ * Rows from seg_offsets[E] on are left untouched. H, F % 16 == 0, H <= 2^20,
+ * E <= 1024; an expert's matrix, and with perm the token rows, below 4 GiB. Outputs
+ * must not overlap inputs or each other. The order of the sums, and with it the bits,
+ * is fixed for a given R_max, shape and device (calls of another R_max may take tiles
+ * of another size).
+ * Workspace: fq_workspace_bytes(FQ_OP_GATED, shape, R_max, 0) (0 bytes: may be NULL).
  * ---------------------------------------------------------------------- */
 fq_status fq_grouped_gated_fwd(const uint16_t *x_bf16, int32_t x_rows, const int32_t *perm,
                                int32_t topk, int32_t R_max, const int32_t *seg_offsets,
@@ -648,8 +652,8 @@ fq_status fq_grouped_gated_bwd(const uint16_t *daq_bf16, const uint16_t *x_bf16,
  *   rsqrt(mean(y^2) + eps), fp32, overwritten, summed in a fixed order.
  *   dx may be dy or dn itself, db may be b itself; outputs must not overlap
  *   otherwise. Workspace, with dw_post or dw_pre: fq_workspace_bytes(FQ_OP_NORM,
- *   {1, T, H}, 0, 0).
- * H % 16 == 0, H <= 16384; bf16 tensors and codes 16-byte aligned; eps > 0.
+ *   {1, T, H}, 0, 0); calls that may overlap on the device need workspaces of their own.
+ * H % 16 == 0, H <= 16384, T * H < 2^34; bf16 tensors and codes 16-byte aligned; eps > 0.
  * ---------------------------------------------------------------------- */
 fq_status fq_norm_residual_fwd(const uint16_t *x_bf16, const uint16_t *b_bf16, const float *gate,
                                float alpha, const uint16_t *w_post_bf16, const uint16_t *w_pre_bf16,

@@ -5,7 +5,8 @@
 //
 // Every function takes the arguments of its C entry point without the stream and
 // with (ws, ws_bytes) as one tensor or None, positionally, and returns the status.
-// Tensors must be contiguous device tensors on the current device; a shape is a
+// Tensors must be contiguous device tensors on the current device, of elements of the
+// C type's size; a shape is a
 // tuple (E, N, K), weights are StoredW, activation quantizers ActQ or None.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -34,7 +35,7 @@ class Args {
   }
   template <class T>
   T *ptr() {
-    return static_cast<T *>(tensor(*a_++));
+    return static_cast<T *>(tensor(*a_++, sizeof(T)));
   }
   int32_t i32() {
     const long v = PyLong_AsLong(*a_++);
@@ -72,8 +73,8 @@ class Args {
     fq_stored_w r{};
     r.fmt = (int32_t)number(w, n_fmt);
     r.group = (int32_t)number(w, n_group);
-    r.codes = field(w, n_codes);
-    r.scale = static_cast<const float *>(field(w, n_scale));
+    r.codes = field(w, n_codes, 1);
+    r.scale = static_cast<const float *>(field(w, n_scale, 4));
     return r;
   }
   // an ActQ or None
@@ -81,13 +82,13 @@ class Args {
     PyObject *a = *a_++;
     if (a == Py_None) return nullptr;
     q.fmt = (int32_t)number(a, n_fmt);
-    q.scale = static_cast<const float *>(field(a, n_scale));
+    q.scale = static_cast<const float *>(field(a, n_scale, 4));
     return &q;
   }
   // a workspace: pointer and size
   void *ws(size_t &bytes) {
     PyObject *o = *a_++;
-    void *p = tensor(o);
+    void *p = tensor(o, 0);
     bytes = p ? THPVariable_Unpack(o).nbytes() : 0;
     return p;
   }
@@ -97,7 +98,8 @@ class Args {
   PyObject *const *a_;
   c10::DeviceIndex dev_;
 
-  void *tensor(PyObject *o) {
+  // elem: bytes of an element (0: any)
+  void *tensor(PyObject *o, size_t elem) {
     if (o == Py_None) return nullptr;
     if (!THPVariable_Check(o)) {
       PyErr_Format(PyExc_TypeError, "a tensor or None is wanted, not %s", Py_TYPE(o)->tp_name);
@@ -117,6 +119,11 @@ class Args {
       PyErr_SetString(PyExc_ValueError, "libfq takes contiguous tensors");
       throw Error{};
     }
+    if (elem && t.element_size() != elem) {
+      PyErr_Format(PyExc_ValueError, "a tensor of %zu-byte elements is wanted, not of %zu bytes", elem,
+                   (size_t)t.element_size());
+      throw Error{};
+    }
     return t.data_ptr();
   }
   PyObject *get(PyObject *o, PyObject *name) {
@@ -131,14 +138,14 @@ class Args {
     if (r == -1 && PyErr_Occurred()) throw Error{};
     return r;
   }
-  void *field(PyObject *o, PyObject *name) {
+  void *field(PyObject *o, PyObject *name, size_t elem) {
     PyObject *v = get(o, name);
     // the object keeps its tensor alive; v is only this look at it
     struct Drop {
       PyObject *p;
       ~Drop() { Py_DECREF(p); }
     } drop{v};
-    return tensor(v);
+    return tensor(v, elem);
   }
 };
 

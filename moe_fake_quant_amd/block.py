@@ -47,7 +47,7 @@ class MoEFakeQuantBlock:
         self.dw_post = torch.empty(H, **f32) if learn_norms and w_post is not None else None
         n = max(256, fq_workspace_bytes(FQ_OP_NORM, (1, T, H), 0, 0)) if learn_norms else 256
         self.ws = torch.empty(n, dtype=torch.uint8, device=layer.dev)
-        self.gate = None
+        self.x = self.gate = None
 
     def _check(self, x: torch.Tensor, gate: Optional[torch.Tensor]) -> int:
         T = x.shape[0]
@@ -65,8 +65,10 @@ class MoEFakeQuantBlock:
     def forward(self, x: torch.Tensor, expert_ids: torch.Tensor, probs: torch.Tensor,
                 gate: Optional[torch.Tensor] = None) -> torch.Tensor:
         """y [T, H]. x is kept by reference for the backward, and gate; neither may be
-        changed before it, nor may x be a buffer that the layer overwrites."""
+        changed before it, nor may x lie in a buffer that the layer overwrites."""
         T = self._check(x, gate)
+        if x.untyped_storage().data_ptr() in self.layer._scratch_at:
+            raise ValueError("x lies in a buffer that the layer overwrites before the backward")
         fq_norm_residual_fwd(x, None, None, 1.0, None, self.w_pre, self.eps, T, self.layer.H, None,
                              self.n[:T])
         b = self.layer.forward(self.n[:T], expert_ids, probs)
@@ -78,6 +80,8 @@ class MoEFakeQuantBlock:
     def backward(self, probs: torch.Tensor, dy: torch.Tensor):
         """dx, and the layer's scale gradients (ds_gu, ds_d); dgate [T], dw_pre and dw_post
         are the block's where they exist."""
+        if self.x is None:
+            raise ValueError("backward needs a forward")
         T, H = self.x.shape[0], self.layer.H
         if dy.shape != (T, H) or dy.dtype != torch.bfloat16:
             raise ValueError(f"dy must be bf16 [{T}, {H}]")

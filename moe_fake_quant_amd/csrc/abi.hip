@@ -242,6 +242,8 @@ fq_status check_product(const void *x, int64_t x_rows, const int32_t *perm, int3
                            : "the int8 product needs N %% 16 == 0 and K %% 16 == 0 (N=%d K=%d)",
                      s.N, s.K);
   FQ_CHECK_SUPPORTED(s.E <= 1024, "up to 1024 experts per stack (E=%d)", s.E);
+  // a tile's 256 direct rows stay within 32-bit offsets of its first
+  FQ_CHECK_SUPPORTED(s.K <= (1 << 20), "rows of up to 2^20 elements (K=%d)", s.K);
   FQ_CHECK_SUPPORTED((size_t)s.N * s.K * elem < (1ull << 32) &&
                          (!perm || (size_t)x_rows * s.K * elem < (1ull << 32)),
                      "an expert's matrix and the token rows must stay below 4 GiB (32-bit offsets)");
@@ -281,6 +283,7 @@ fq_status check_norm(int32_t T, int32_t H, const uint16_t *b, const float *gate,
                      const uint16_t *w_post, const uint16_t *w_pre, float eps) {
   FQ_CHECK_ARG(T >= 0 && H > 0 && H % 16 == 0, "bad sizes (T=%d H=%d; H %% 16 == 0)", T, H);
   FQ_CHECK_SUPPORTED(H <= kNormMaxRow, "rows of up to %d elements (H=%d)", kNormMaxRow, H);
+  FQ_CHECK_ARG((int64_t)T * H < (1ll << 34), "too many elements");
   FQ_CHECK_ARG(eps > 0.0f && eps <= 3.4028235e38f, "eps must be finite and > 0");
   FQ_CHECK_ARG(alpha - alpha == 0.0f, "alpha must be finite");
   FQ_CHECK_ARG(b || (!gate && !w_post), "gate and w_post belong to a block output b");
@@ -978,6 +981,7 @@ fq_status fq_swiglu_bwd_ckpt(const uint16_t *daq, const uint8_t *codes, const fl
 fq_status fq_quantize_tokens(const uint16_t *x, int32_t rows, int32_t K, const int32_t *n_rows,
                              uint8_t *codes, float *scale, fq_stream stream) {
   FQ_CHECK_ARG(rows >= 0 && K > 0 && K % 16 == 0, "bad sizes (rows=%d K=%d; K %% 16 == 0)", rows, K);
+  FQ_CHECK_ARG((int64_t)rows * K < (1ll << 35), "too many elements");
   FQ_CHECK_ARG(rows == 0 || (x && codes && scale), "NULL pointer");
   FQ_CHECK_ARG((!x || aligned16(x)) && (!codes || aligned16(codes)),
                "x and codes must be 16-byte aligned");

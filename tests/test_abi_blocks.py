@@ -34,7 +34,7 @@ INT8_BAD = [(dict(x=None), INVALID), (dict(sx=None), INVALID), (dict(seg=None), 
             (dict(sx=P + 2), INVALID), (dict(shape=(0, 32, 64)), INVALID), (dict(shape=(2, 24, 64)), UNSUPPORTED),
             (dict(shape=(2, 32, 72)), UNSUPPORTED), (dict(shape=(1025, 32, 64)), UNSUPPORTED),
             (dict(shape=(1, 1 << 17, 1 << 15)), INVALID),
-            (dict(perm=P, rows=1 << 27), UNSUPPORTED)]
+            (dict(perm=P, rows=1 << 27), UNSUPPORTED), (dict(shape=(1, 32, 1 << 21)), UNSUPPORTED)]
 
 
 @host_only
@@ -81,7 +81,8 @@ GATED_BAD = [(dict(x=None), INVALID), (dict(seg=None), INVALID), (dict(out=None)
              (dict(rows=3), INVALID), (dict(perm=P, topk=-1), INVALID), (dict(fmt=2, scale=P), INVALID),
              (dict(fmt=3), INVALID), (dict(fmt=9, scale=P), INVALID), (dict(shape=(2, 16, 64)), UNSUPPORTED),
              (dict(shape=(2, 64, 8)), UNSUPPORTED), (dict(shape=(1025, 64, 64)), UNSUPPORTED),
-             (dict(shape=(1, 1 << 16, 1 << 15)), UNSUPPORTED), (dict(perm=P, rows=1 << 26), UNSUPPORTED)]
+             (dict(shape=(1, 1 << 16, 1 << 15)), UNSUPPORTED), (dict(perm=P, rows=1 << 26), UNSUPPORTED),
+             (dict(shape=(1, 64, 1 << 21)), UNSUPPORTED)]
 
 
 @host_only
@@ -109,7 +110,8 @@ def test_quantize_tokens_refuses(pkg):  # noqa: F811
                          ((P, 4, 64, None, P, None), INVALID), ((P, -1, 64, None, P, P), INVALID),
                          ((P, 4, 24, None, P, P), INVALID), ((P, 4, 0, None, P, P), INVALID),
                          ((P + 2, 4, 64, None, P, P), INVALID), ((P, 4, 64, None, P + 1, P), INVALID),
-                         ((P, 4, 64, None, P, P + 2), INVALID), ((None, 0, 64, None, None, None), 0)):
+                         ((P, 4, 64, None, P, P + 2), INVALID),
+                         ((P, 1 << 30, 64, None, P, P), INVALID), ((None, 0, 64, None, None, None), 0)):
         assert call(pkg, "fq_quantize_tokens", args + (None,))[0] == status, args
 
 
@@ -127,7 +129,7 @@ def norm_bwd(**kw):
     return tuple(a.values()) + (None,)
 
 
-SHARED_BAD = [(dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(H=24), INVALID), (dict(H=16400), UNSUPPORTED),
+SHARED_BAD = [(dict(T=1 << 30), INVALID), (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(H=24), INVALID), (dict(H=16400), UNSUPPORTED),
               (dict(eps=0.0), INVALID), (dict(eps=NAN), INVALID), (dict(eps=INF), INVALID),
               (dict(alpha=INF), INVALID), (dict(alpha=NAN), INVALID), (dict(b=None), INVALID),
               (dict(b=P + 8), INVALID), (dict(w_post=P + 2), INVALID), (dict(w_pre=P + 2), INVALID)]

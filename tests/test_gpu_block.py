@@ -245,15 +245,30 @@ def test_block_over_int8_codes_and_replays():
     with torch.cuda.graph(g):
         out = blk.forward_int8(x, ids, p, gate)
     train, tx, tids, tp, tdy = make(O.FMT_FP8, O.FMT_FP8, None, recompute=True)
-    tb = block_of(train)
+    tb = block_of(train, learn_norms=True)
+
+    def step():
+        train.quantize_weights()
+        tb.forward(tx, tids, tp)
+        return (*tb.backward(tp, tdy), tb.dw_pre, tb.dw_post)
+
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    gt = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gt):
+        touts = step()
     first = None
     for rep in range(3):
         x.copy_(torch.randn(x.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(rep)).bfloat16())
-        train.quantize_weights()
-        tb.forward(tx, tids, tp)
-        got = bits(*tb.backward(tp, tdy))
+        got = bits(*step())
         first = first or got
         assert same(got, first)
+        for t in touts:
+            t.zero_()
+        gt.replay()
+        assert same(bits(*touts), first)
         out.zero_()
         g.replay()
         got = bits(out)
@@ -265,6 +280,10 @@ def test_block_refusals():
     with pytest.raises(ValueError):
         F.MoEFakeQuantBlock(layer, torch.ones(layer.H, device="cuda"))
     blk = block_of(layer)
+    with pytest.raises(ValueError):
+        blk.backward(p, dy)
+    with pytest.raises(ValueError):
+        blk.forward(layer.out, ids, p)
     for bad in ((x[:, :64], None), (x.float(), None), (torch.cat((x, x)), None), (x, torch.ones(3, device="cuda"))):
         with pytest.raises(ValueError):
             blk.forward(bad[0], ids, p, bad[1])
@@ -279,6 +298,8 @@ def test_another_device_and_layouts_are_refused():
     for bad in (x.cpu(), x.t(), torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")[:, ::2]):
         with pytest.raises(ValueError):
             F.fq_norm_residual_fwd(bad, None, None, 1.0, None, w, 1e-6, 4, 32, None, torch.empty_like(x))
+    with pytest.raises(ValueError):
+        F.fq_norm_residual_fwd(x.float(), None, None, 1.0, None, w, 1e-6, 4, 32, None, torch.empty_like(x))
     with pytest.raises(TypeError):
         F.fq_norm_residual_fwd(x.data_ptr(), None, None, 1.0, None, w, 1e-6, 4, 32, None, torch.empty_like(x))
     with pytest.raises(F.FQError):
