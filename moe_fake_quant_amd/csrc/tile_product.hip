@@ -14,13 +14,18 @@
 // no exchange but the amax of an NVFP4 block between the lane halves, and h never
 // leaves the registers.
 //
-// A stage takes 1.0 to 1.5 us for its 64 KB, and the matrix unit is busy 46 to 49 % of
-// the time (bf16) or 28 % (int8 with a contraction of 768): the operands' way from L2
-// through L1 into LDS bounds it, and at 768 the epilogue, which a CU's only block
-// cannot hide. Loads of a later stage issued ahead into L2 made it 30 % slower. Measured
-// with 128 experts, the kernel alone: gated forward over 65536 rows, H 2048, F 768, FP8
-// 443 us (931 TFLOP/s); its backward over 131072 rows 860 us (959 TFLOP/s); int8 over
-// 131072 rows of [2048 x 768] 335 us (1.23 POP/s).
+// A stage takes about 1.8 us, twice what its MFMAs need (the matrix unit is busy 46 to
+// 49 % of the time), for both types and also where all operands lie in L2; a tile has
+// 5 to 7 us around its stages (28 % busy for int8 with a contraction of 768). The
+// operands' way through L1 into LDS bounds it, not the LDS reads or the barriers: four
+// waves of 128 x 128, with two thirds of the LDS reads and half the barriers, took as
+// long a stage (and 10 to 20 % more in all, for a longer epilogue). Without its stores
+// the kernel takes 4 % (gated) to 20 % (int8, 768) less. Loads of a later stage issued
+// ahead into L2 made it 30 % slower; eighths of the experts starting at different
+// stages, 15 % faster at 128 rows of bf16 an expert and 2 % slower at 512 and more.
+// Measured with 128 experts, the kernel alone: gated forward over 65536 rows, H 2048, F
+// 768, FP8 443 us (931 TFLOP/s); its backward over 131072 rows 860 us (959 TFLOP/s);
+// int8 over 131072 rows of [2048 x 768] 335 us (1.23 POP/s).
 //
 // Rows and columns past the ends are clamped in the load addresses and not stored.
 // A contraction that ends inside a stage: the loading wave overwrites the chunks
