@@ -21,6 +21,14 @@ from . import (FQ_OP_NORM, fq_norm_residual_bwd, fq_norm_residual_fwd, fq_worksp
 from .layer import MoEFakeQuantLayer
 
 
+def _at(t: torch.Tensor) -> int:
+    return t.untyped_storage().data_ptr()
+
+
+def _in(t: torch.Tensor, *buffers: torch.Tensor) -> bool:
+    return any(_at(t) == _at(b) for b in buffers)
+
+
 class MoEFakeQuantBlock:
     def __init__(self, layer: MoEFakeQuantLayer, w_pre: torch.Tensor,
                  w_post: Optional[torch.Tensor] = None, alpha: float = 1.0, eps: float = 1e-6,
@@ -65,10 +73,11 @@ class MoEFakeQuantBlock:
     def forward(self, x: torch.Tensor, expert_ids: torch.Tensor, probs: torch.Tensor,
                 gate: Optional[torch.Tensor] = None) -> torch.Tensor:
         """y [T, H]. x is kept by reference for the backward, and gate; neither may be
-        changed before it, nor may x lie in a buffer that the layer overwrites."""
+        changed before it, nor may x lie in a buffer that the layer or the block overwrites."""
         T = self._check(x, gate)
-        if x.untyped_storage().data_ptr() in self.layer._scratch_at:
-            raise ValueError("x lies in a buffer that the layer overwrites before the backward")
+        if _in(x, self.y, self.n, self.b, self.db, self.dx) or _at(x) in self.layer._scratch_at:
+            raise ValueError("x lies in a buffer that the layer or the block overwrites before the "
+                             "backward")
         fq_norm_residual_fwd(x, None, None, 1.0, None, self.w_pre, self.eps, T, self.layer.H, None,
                              self.n[:T])
         b = self.layer.forward(self.n[:T], expert_ids, probs)
@@ -85,6 +94,8 @@ class MoEFakeQuantBlock:
         T, H = self.x.shape[0], self.layer.H
         if dy.shape != (T, H) or dy.dtype != torch.bfloat16:
             raise ValueError(f"dy must be bf16 [{T}, {H}]")
+        if _in(dy, self.db) or _at(dy) in self.layer._scratch_at:
+            raise ValueError("dy lies in a buffer that the layer's backward overwrites")
         fq_norm_residual_bwd(dy, None, None, self.b[:T], self.gate, self.alpha, self.w_post, None,
                              self.eps, T, H, None, self.db[:T],
                              None if self.gate is None else self.dgate[:T], self.dw_post, None, self.ws)
@@ -99,6 +110,8 @@ class MoEFakeQuantBlock:
         as codes with a scale a token and is never stored in bf16."""
         T = self._check(x, gate)
         self.layer._check_int8()
+        if _in(x, self.layer.i8["out"]):
+            raise ValueError("x lies in the buffer that the layer's output overwrites")
         codes, scale = self.layer.i8["x_codes"], self.layer.i8["x_scale"]
         fq_norm_residual_fwd(x, None, None, 1.0, None, self.w_pre, self.eps, T, self.layer.H, None, None,
                              codes, scale)

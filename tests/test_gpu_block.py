@@ -306,3 +306,29 @@ def test_another_device_and_layouts_are_refused():
         F.fq_norm_residual_fwd(x, None, None, 1.0, None, w, 0.0, 4, 32, None, torch.empty_like(x))
     with pytest.raises(OverflowError):
         F.fq_norm_residual_fwd(x, None, None, 1.0, None, w, 1e-6, 1 << 40, 32, None, torch.empty_like(x))
+
+
+def test_block_refuses_inputs_that_its_own_calls_overwrite():
+    """A block's or its layer's own buffers: as x of a training step (kept until the
+    backward), as dy, and the int8 layer's output as x of the int8 form."""
+    layer, x, ids, p, dy = make(O.FMT_INT8, O.FMT_INT8, None)
+    T = x.shape[0]
+    blk = block_of(layer)
+    layer.quantize_weights()
+    y = blk.forward(x, ids, p)
+    for bad in (y, blk.dx[:T], layer.out[:T]):
+        with pytest.raises(ValueError):
+            blk.forward(bad, ids, p)
+    for bad in (blk.db[:T], layer.dx[:T]):
+        with pytest.raises(ValueError):
+            blk.backward(p, bad)
+    first = bits(blk.backward(p, dy)[0])
+    blk.dx[:T].copy_(dy)  # the block's own dx may be dy
+    assert same(bits(blk.backward(p, blk.dx[:T])[0]), first)
+    layer.export()
+    z = layer.forward_int8(x, ids, p)
+    with pytest.raises(ValueError):
+        blk.forward_int8(z, ids, p)
+    want = bits(blk.forward_int8(x, ids, p))
+    blk.y[:T].copy_(x)  # in place on the block's own y
+    assert same(bits(blk.forward_int8(blk.y[:T], ids, p)), want)
