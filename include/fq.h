@@ -579,8 +579,8 @@ fq_status fq_swiglu_bwd_ckpt(const uint16_t *daq_bf16, const uint8_t *codes, con
  * fq_grouped_gated_int8: shape {E, 2F, H}: g and u such sums over rows f and
  *   F + f of the stack, a[r, f] = bf16(silu(g) * u) [R_max, F].
  *   x_codes [x_rows, K], x_scale [x_rows]. perm NULL: routed row r is row r of x
- *   (x_rows >= R_max); else row perm[r] / topk of x (perm as fq_moe_permute
- *   gives it, x_rows = T). w: FQ_FMT_INT8 codes [E, N, K] as exported, group = K
+ *   (x_rows >= R_max; topk is not read); else row perm[r] / topk of x (perm as
+ *   fq_moe_permute gives it, x_rows = T). w: FQ_FMT_INT8 codes [E, N, K] as exported, group = K
  *   (scale [E, N]) or FQ_GROUP_TENSOR (scale [E]); the other fields unused.
  *   Rows from seg_offsets[E] on are left untouched.
  * K and N (gated: F) multiples of 16, K <= 131071, E <= 1024; an expert's codes,

@@ -203,7 +203,8 @@ static ProdArgs prod_args(const void *x, const int32_t *perm, int topk, const in
   a.w = static_cast<const char *>(w);
   a.x = static_cast<const char *>(x);
   a.perm = perm;
-  a.topk = FastDiv((uint32_t)topk);
+  // direct rows have no topk (a division by any value that the caller left there)
+  a.topk = perm ? FastDiv((uint32_t)topk) : FastDiv();
   a.seg = seg;
   a.E = s.E;
   a.N = s.N;

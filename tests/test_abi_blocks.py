@@ -2,6 +2,9 @@
 rejected by the host checks before anything is enqueued, so the placeholder
 addresses are never read (run where no GPU is visible)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -169,3 +172,27 @@ def test_workspace_sizes(pkg):  # noqa: F811
 def test_native_marshalling_checks_its_arguments(pkg):  # noqa: F811
     with pytest.raises(TypeError):
         pkg._b.fq_quantize_tokens(None, 0)
+
+
+DIRECT = """
+import ctypes
+import moe_fake_quant_amd as pkg
+P = 1 << 12
+lib, sh = pkg.lib(), pkg.fq_shape(2, 64, 64)
+w = ctypes.byref(pkg.fq_stored_w(1, 64, P, P, None, None, None))
+for topk in (0, -1):
+    for fn in ("fq_grouped_gemm_int8", "fq_grouped_gated_int8"):
+        print(getattr(lib, fn)(P, P, 8, None, topk, 8, P, sh, w, P, None, 0, None))
+    print(lib.fq_grouped_gated_fwd(P, 8, None, topk, 8, P, sh, P, None, P, None, 0, None))
+    print(lib.fq_grouped_gated_bwd(P, P, 8, None, topk, 8, P, sh, P, None, P, None, None, 0, None))
+"""
+
+
+@host_only
+def test_direct_rows_do_not_read_topk(pkg):  # noqa: F811
+    """Without perm any topk passes the checks: the calls get as far as the launch, which
+    fails here without a device (in a process of its own, which an arithmetic trap would end)."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", DIRECT], capture_output=True, text=True, cwd=root)
+    assert r.returncode == 0, (r.returncode, r.stderr[-500:])
+    assert r.stdout.split() == ["4"] * 8, r.stdout

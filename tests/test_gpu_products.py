@@ -371,6 +371,27 @@ def test_repeats_streams_and_replays_are_bitwise_equal(T, H, Fc):
         assert same(one, cap), f"replay {rep}"
 
 
+@pytest.mark.parametrize("T", [5, 300, 3000])
+def test_direct_rows_do_not_read_topk(T):
+    """topk 0 without perm: the bits of topk 1."""
+    rng = np.random.default_rng(T)
+    H, Fc = 96, 272
+    x, w, d = (dev_bf16(normal_bits(rng, *s)) for s in ((T, H), (2, 2 * Fc, H), (T, Fc)))
+    xc, sx = dev_u8(codes(rng, T, H)), dev_f32(rng.random(T))
+    st = F.StoredW(F.FMT_INT8, H, dev_u8(codes(rng, 2, 2 * Fc, H)), dev_f32(rng.random((2, 2 * Fc))))
+    seg, shape = dev_i32([0, T // 3, T]), (2, 2 * Fc, H)
+
+    def run(topk):
+        y, a, aq, dh = out_bf16(T, 2 * Fc), out_bf16(T, Fc), out_bf16(T, Fc), out_bf16(T, 2 * Fc)
+        F.fq_grouped_gemm_int8(xc, sx, T, None, topk, T, seg, shape, st, y)
+        F.fq_grouped_gated_int8(xc, sx, T, None, topk, T, seg, shape, st, a)
+        F.fq_grouped_gated_fwd(x, T, None, topk, T, seg, shape, w, None, aq)
+        F.fq_grouped_gated_bwd(d, x, T, None, topk, T, seg, shape, w, None, dh)
+        return [t.view(torch.int16) for t in (y, a, aq, dh)]
+
+    assert all(torch.equal(p, q) for p, q in zip(run(0), run(1)))
+
+
 def test_direct_rows_past_4_gib():
     """Direct rows are not bound to 32-bit offsets: the last rows of an x of more than
     4 GiB."""
