@@ -653,7 +653,9 @@ fq_status fq_grouped_gated_bwd(const uint16_t *daq_bf16, const uint16_t *x_bf16,
  *   dx may be dy or dn itself, db may be b itself; outputs must not overlap
  *   otherwise. Workspace, with dw_post or dw_pre: fq_workspace_bytes(FQ_OP_NORM,
  *   {1, T, H}, 0, 0); calls that may overlap on the device need workspaces of their own.
- * H % 16 == 0, H <= 16384, T * H < 2^34; bf16 tensors and codes 16-byte aligned; eps > 0.
+ * H % 16 == 0, H <= 16384, T * H < 2^34; bf16 tensors and codes 16-byte aligned;
+ * eps > 0. The sums of squares are fp32: a row whose own passes 2^128 (elements of
+ * about 1e17 and more) has no norm here.
  * ---------------------------------------------------------------------- */
 fq_status fq_norm_residual_fwd(const uint16_t *x_bf16, const uint16_t *b_bf16, const float *gate,
                                float alpha, const uint16_t *w_post_bf16, const uint16_t *w_pre_bf16,

@@ -7,10 +7,10 @@
 // n leaves as bf16 or as int8 codes with one scale a token (the operand of the
 // int8 product). n is formed from the unrounded y.
 // Backward, from the stored y, with v = dn * w_pre and q = alpha * gate_t:
-//   gy = dy + ry * (v - y * ry^2 * mean(v y))              -> dx
+//   gy = dy + ry * (v - (y ry) * mean(v y) ry)             -> dx
 //   dw_pre = sum_t dn y ry
 //   S = sum_h gy b w_post     dgate = alpha rb S
-//   db = q rb (gy w_post - b rb^2 S / H)    (w_post NULL: db = q gy)
+//   db = q rb (gy w_post - (b rb) rb S / H) (w_post NULL: db = q gy)
 //   dw_post = sum_t q gy b rb
 // so one pass takes three row sums (y^2, v y, b^2) and, from registers, a fourth (S).
 //
@@ -181,7 +181,9 @@ __global__ __launch_bounds__(kRowThreads<WPR>) void k_norm_bwd(NormArgs a) {
     }
     row_sum<WPR>(s, red[flip]);
     const float ry = a.dn ? rsqrtf(s[0] * a.inv_h + a.eps) : 0.0f;
-    const float ky = ry * ry * ry * (s[1] * a.inv_h);
+    // mean(v y) ry: with y ry beside it no power of the root is formed, which would leave
+    // fp32's range before the row's sum of squares does (rows about 1e15 large, eps below 1e-26)
+    const float my = ry * (s[1] * a.inv_h);
     const float rb = a.w_post ? rsqrtf(s[2] * a.inv_h + a.eps) : 1.0f;
     const float q = a.b ? a.alpha * (a.gate ? a.gate[t] : 1.0f) : 0.0f;
     float gy[VPT][8];
@@ -198,8 +200,9 @@ __global__ __launch_bounds__(kRowThreads<WPR>) void k_norm_bwd(NormArgs a) {
           unpack8(a.w_pre[c], w);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            gy[i][j] += fmaf(ry, dn[j] * w[j], -(ky * y[j]));
-            if (DW) ap[i][j] = fmaf(dn[j], y[j] * ry, ap[i][j]);
+            const float yr = y[j] * ry;
+            gy[i][j] = fmaf(ry, fmaf(-my, yr, dn[j] * w[j]), gy[i][j]);
+            if (DW) ap[i][j] = fmaf(dn[j], yr, ap[i][j]);
           }
         }
         if (a.dx) a.dx[row + c] = pack8(gy[i]);
@@ -219,7 +222,7 @@ __global__ __launch_bounds__(kRowThreads<WPR>) void k_norm_bwd(NormArgs a) {
     row_sum<WPR>(sb, red[flip] + 3 * WPR);
     if (a.dgate && lane == 0) a.dgate[t] = a.alpha * (rb * sb[0]);
     if (a.db) {
-      const float kb = a.w_post ? rb * rb * (sb[0] * a.inv_h) : 0.0f;
+      const float mb = rb * (sb[0] * a.inv_h);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int c = lane + i * WPR * 64;
@@ -229,7 +232,7 @@ __global__ __launch_bounds__(kRowThreads<WPR>) void k_norm_bwd(NormArgs a) {
           if (a.w_post) unpack8(a.w_post[c], w);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            o[j] = a.w_post ? (q * rb) * fmaf(gy[i][j], w[j], -(kb * b[j])) : q * gy[i][j];
+            o[j] = a.w_post ? (q * rb) * fmaf(-mb, b[j] * rb, gy[i][j] * w[j]) : q * gy[i][j];
           a.db[row + c] = pack8(o);
         }
       }
