@@ -48,8 +48,8 @@ template <int WPR, int VPT>
 __global__ __launch_bounds__(kRowThreads<WPR>) void k_norm_fwd(NormArgs a) {
   __shared__ float red[3 * WPR];
   const int lane = threadIdx.x & (WPR * 64 - 1);
-  const int t = blockIdx.x * kBlockRows<WPR> + threadIdx.x / (WPR * 64);
-  if (t >= a.T) return;  // whole rows: with WPR > 1 the whole block
+  const uint32_t t = grid_row<WPR>();
+  if (t >= (uint32_t)a.T) return;  // whole rows: with WPR > 1 the whole block
   const size_t row = (size_t)t * a.nv;
   bf16x8_t vx[VPT], vb[VPT];
 #pragma unroll
@@ -301,8 +301,8 @@ __global__ __launch_bounds__(kRowThreads<WPR>) void k_quantize_tokens(const bf16
   __shared__ uint32_t red[WPR];
   if (n_rows) rows = min(rows, n_rows[0]);
   const int lane = threadIdx.x & (WPR * 64 - 1);
-  const int t = blockIdx.x * kBlockRows<WPR> + threadIdx.x / (WPR * 64);
-  if (t >= rows) return;
+  const uint32_t t = grid_row<WPR>();
+  if ((int64_t)t >= rows) return;  // (n_rows may be negative)
   const size_t row = (size_t)t * nv;
   bf16x8_t v[VPT];
   uint32_t top = 0;
@@ -386,8 +386,8 @@ void launch_norm_fwd(const uint16_t *x, const uint16_t *b, const float *gate, fl
   a.scale = scale;
   with_row_form(H, [&](auto wpr, auto vpt) {
     constexpr int W = decltype(wpr)::value, V = decltype(vpt)::value;
-    hipLaunchKernelGGL((k_norm_fwd<W, V>), dim3(ceil_div(T, kBlockRows<W>)), dim3(kRowThreads<W>), 0, st,
-                       a);
+    hipLaunchKernelGGL((k_norm_fwd<W, V>), row_grid(ceil_div(T, kBlockRows<W>)), dim3(kRowThreads<W>), 0,
+                       st, a);
   });
 }
 
@@ -419,7 +419,9 @@ void launch_norm_bwd(const uint16_t *dy, const uint16_t *dn, const uint16_t *y, 
       hipLaunchKernelGGL((k_norm_bwd<W, V, true>), dim3(nb), threads, W == 1 ? (size_t)4 * H * 4 : 0, st,
                          a);
     else
-      hipLaunchKernelGGL((k_norm_bwd<W, V, false>), dim3(ceil_div(T, kBlockRows<W>)), threads, 0, st, a);
+      // (the kernel strides over the rows: along x alone)
+      hipLaunchKernelGGL((k_norm_bwd<W, V, false>), dim3(row_grid(ceil_div(T, kBlockRows<W>)).x), threads, 0,
+                         st, a);
   });
   if (dw)
     hipLaunchKernelGGL(k_norm_dw, dim3((H + 31) / 32, 2), dim3(1024), 0, st, a.part_post, a.part_pre, nb, H,
@@ -431,11 +433,11 @@ void launch_quantize_tokens(const uint16_t *x, int rows, int K, const int32_t *n
   const bf16x8_t *v = reinterpret_cast<const bf16x8_t *>(x);
   uint2 *c = reinterpret_cast<uint2 *>(codes);
   if (K <= 1024)
-    hipLaunchKernelGGL((k_quantize_tokens<1, 2>), dim3((rows + 3) / 4), dim3(256), 0, st, v, rows, K / 8,
-                       n_rows, c, scale);
+    hipLaunchKernelGGL((k_quantize_tokens<1, 2>), row_grid(ceil_div(rows, 4)), dim3(256), 0, st, v, rows,
+                       K / 8, n_rows, c, scale);
   else
-    hipLaunchKernelGGL((k_quantize_tokens<4, 4>), dim3(rows), dim3(256), 0, st, v, rows, K / 8, n_rows, c,
-                       scale);
+    hipLaunchKernelGGL((k_quantize_tokens<4, 4>), row_grid(rows), dim3(256), 0, st, v, rows, K / 8, n_rows,
+                       c, scale);
 }
 
 }  // namespace fq
