@@ -651,7 +651,8 @@ fq_status fq_grouped_gated_bwd(const uint16_t *daq_bf16, const uint16_t *x_bf16,
  *   dw_post[h] = sum_t dp b rsqrt(mean(b^2) + eps), dw_pre[h] = sum_t dn y
  *   rsqrt(mean(y^2) + eps), fp32, overwritten, summed in a fixed order.
  *   dx may be dy or dn itself, db may be b itself; outputs must not overlap
- *   otherwise. Workspace, with dw_post or dw_pre: fq_workspace_bytes(FQ_OP_NORM,
+ *   otherwise. T == 0: nothing but dw_post and dw_pre (0) is written, and the row
+ *   tensors of either call may be NULL. Workspace, with dw_post or dw_pre: fq_workspace_bytes(FQ_OP_NORM,
  *   {1, T, H}, 0, 0); calls that may overlap on the device need workspaces of their own.
  * H % 16 == 0, H <= 16384, T * H < 2^34; bf16 tensors and codes 16-byte aligned;
  * eps > 0. The sums of squares are fp32: a row whose own passes 2^128 (elements of

@@ -286,7 +286,8 @@ fq_status check_norm(int32_t T, int32_t H, const uint16_t *b, const float *gate,
   FQ_CHECK_ARG((int64_t)T * H < (1ll << 34), "too many elements");
   FQ_CHECK_ARG(eps > 0.0f && eps <= 3.4028235e38f, "eps must be finite and > 0");
   FQ_CHECK_ARG(alpha - alpha == 0.0f, "alpha must be finite");
-  FQ_CHECK_ARG(b || (!gate && !w_post), "gate and w_post belong to a block output b");
+  // (without rows the row tensors have no address)
+  FQ_CHECK_ARG(b || T == 0 || (!gate && !w_post), "gate and w_post belong to a block output b");
   FQ_CHECK_ARG((!b || aligned16(b)) && (!w_post || aligned16(w_post)) && (!w_pre || aligned16(w_pre)),
                "bf16 tensors must be 16-byte aligned");
   return FQ_OK;
@@ -1052,10 +1053,10 @@ fq_status fq_norm_residual_fwd(const uint16_t *x, const uint16_t *b, const float
                                fq_stream stream) {
   FQ_TRY(check_norm(T, H, b, gate, alpha, w_post, w_pre, eps));
   FQ_CHECK_ARG(T == 0 || x, "x is NULL");
-  FQ_CHECK_ARG(y || n || codes, "no output");
+  FQ_CHECK_ARG(y || n || codes || T == 0, "no output");
   FQ_CHECK_ARG(w_pre || (!n && !codes), "n and codes need w_pre");
-  FQ_CHECK_ARG(!w_pre || n || codes, "w_pre needs n or codes");
-  FQ_CHECK_ARG(!codes == !scale, "codes and scale go together");
+  FQ_CHECK_ARG(!w_pre || n || codes || T == 0, "w_pre needs n or codes");
+  FQ_CHECK_ARG(!codes == !scale || T == 0, "codes and scale go together");
   FQ_CHECK_ARG((!x || aligned16(x)) && (!y || aligned16(y)) && (!n || aligned16(n)) &&
                    (!codes || aligned16(codes)) && (reinterpret_cast<uintptr_t>(scale) & 3u) == 0,
                "tensors must be 16-byte aligned (scale: 4)");
@@ -1071,17 +1072,18 @@ fq_status fq_norm_residual_bwd(const uint16_t *dy, const uint16_t *dn, const uin
                                int32_t H, uint16_t *dx, uint16_t *db, float *dgate, float *dw_post,
                                float *dw_pre, void *ws, size_t ws_bytes, fq_stream stream) {
   FQ_TRY(check_norm(T, H, b, gate, alpha, w_post, w_pre, eps));
-  FQ_CHECK_ARG(dx || db || dgate || dw_post || dw_pre, "no output");
+  FQ_CHECK_ARG(dx || db || dgate || dw_post || dw_pre || T == 0, "no output");
   FQ_CHECK_ARG(dy || dn || T == 0, "dy and dn are both NULL");
   FQ_CHECK_ARG(!dn || (y && w_pre) || T == 0, "dn needs y and w_pre");
   FQ_CHECK_ARG(!dw_pre || w_pre, "dw_pre needs w_pre");
   FQ_CHECK_ARG(!dw_pre || dn || T == 0, "dw_pre needs dn");
   FQ_CHECK_ARG(b || T == 0 || (!db && !dgate && !dw_post), "db, dgate and dw_post need b");
   FQ_CHECK_ARG(!dw_post || w_post, "dw_post needs w_post");
-  FQ_CHECK_ARG(!dgate || gate, "dgate needs gate");
+  FQ_CHECK_ARG(!dgate || gate || T == 0, "dgate needs gate");
   FQ_CHECK_ARG((!dy || aligned16(dy)) && (!dn || aligned16(dn)) && (!y || aligned16(y)) &&
                    (!dx || aligned16(dx)) && (!db || aligned16(db)),
                "bf16 tensors must be 16-byte aligned");
+  if (T == 0 && !dw_post && !dw_pre) return FQ_OK;
   const size_t need = dw_post || dw_pre ? align_up(norm_ws_bytes(T, H)) : 0;
   if (need > 0 && (!ws || ws_bytes < need)) {
     set_error("fq_norm_residual_bwd: workspace %zu bytes < %zu needed", ws_bytes, need);

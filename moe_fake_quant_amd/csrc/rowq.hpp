@@ -14,9 +14,8 @@ constexpr int kRowThreads = WPR == 1 ? 256 : WPR * 64;
 template <int WPR>
 constexpr int kBlockRows = WPR == 1 ? 4 : 1;
 
-// One block a kBlockRows rows. A grid of 2^32 or more threads along x loses its last blocks
-// without an error, and short rows reach that
-// (2^26 rows of one wave each): the blocks beyond 2^22 go along y.
+// One block a kBlockRows rows. A grid of 2^32 or more threads along x loses blocks without an
+// error, and short rows reach that (2^26 of one wave each): blocks beyond 2^22 go along y.
 inline dim3 row_grid(int blocks) {
   constexpr int kX = 1 << 22;
   return blocks <= kX ? dim3(blocks) : dim3(kX, ceil_div(blocks, kX));

@@ -196,3 +196,16 @@ def test_direct_rows_do_not_read_topk(pkg):  # noqa: F811
     r = subprocess.run([sys.executable, "-c", DIRECT], capture_output=True, text=True, cwd=root)
     assert r.returncode == 0, (r.returncode, r.stderr[-500:])
     assert r.stdout.split() == ["4"] * 8, r.stdout
+
+
+@host_only
+def test_norms_without_rows(pkg):  # noqa: F811
+    """Empty tensors have no address: with T = 0 every row tensor may be NULL, and nothing is
+    enqueued without the weights' gradients."""
+    rows = dict(T=0, x=None, b=None, gate=None, y=None, n=None)
+    for kw in (rows, dict(rows, w_post=None), dict(rows, w_pre=None), dict(rows, codes=P)):
+        assert call(pkg, "fq_norm_residual_fwd", norm_fwd(**kw))[0] == 0, kw
+    rows = dict(T=0, dy=None, dn=None, y=None, b=None, gate=None, dx=None, db=None, dgate=None)
+    for kw in (rows, dict(rows, w_post=None), dict(rows, w_pre=None)):
+        assert call(pkg, "fq_norm_residual_bwd", norm_bwd(**kw))[0] == 0, kw
+    assert call(pkg, "fq_norm_residual_fwd", norm_fwd(T=0, H=24))[0] == INVALID

@@ -332,3 +332,20 @@ def test_block_refuses_inputs_that_its_own_calls_overwrite():
     want = bits(blk.forward_int8(x, ids, p))
     blk.y[:T].copy_(x)  # in place on the block's own y
     assert same(bits(blk.forward_int8(blk.y[:T], ids, p)), want)
+
+
+@pytest.mark.parametrize("post,gated", [(True, True), (False, False)])
+@pytest.mark.parametrize("mode", [dict(), dict(recompute=True), dict(ckpt=(O.FMT_INT8, 64))])
+def test_block_without_tokens(post, gated, mode):
+    """A rank that no token reaches: empty results, and weights' gradients of zero."""
+    layer, x, ids, p, dy = make(O.FMT_INT8, O.FMT_INT8, None, **mode)
+    blk = block_of(layer, post, learn_norms=True)
+    gate = torch.ones(0, device="cuda") if gated else None
+    layer.quantize_weights()
+    layer.export()
+    blk.dw_pre.fill_(7.0)
+    assert blk.forward(x[:0], ids[:0], p[:0], gate).shape == (0, layer.H)
+    dx, ds_gu, ds_d = blk.backward(p[:0], dy[:0])
+    assert dx.shape == (0, layer.H) and not ds_gu.any() and not ds_d.any() and not blk.dw_pre.any()
+    assert not post or not blk.dw_post.any()
+    assert blk.forward_int8(x[:0], ids[:0], p[:0], gate).shape == (0, layer.H)
