@@ -615,8 +615,8 @@ fq_status fq_grouped_gated_int8(const uint8_t *x_codes, const float *x_scale, in
  * shape {E, 2F, H}; w_fq [E, 2F, H] bf16, used as given (fq_quantize_stacked's
  * output, or the raw weights). x_bf16 [x_rows, H] already fake-quantized, read
  * through perm / topk or (perm NULL) by routed row, as for the int8 products.
- * Rows from seg_offsets[E] on are left untouched. H, F % 16 == 0, H <= 2^20,
- * E <= 1024; an expert's matrix, and with perm the token rows, below 4 GiB. Outputs
+ * Rows from seg_offsets[E] on are left untouched. H, F % 16 == 0, H <= 2^20, F <= 2^25
+ * in the backward, E <= 1024; an expert's matrix, and with perm the token rows, below 4 GiB. Outputs
  * must not overlap inputs or each other. The order of the sums, and with it the bits,
  * is fixed for a given R_max, shape and device (calls of another R_max may take tiles
  * of another size).

@@ -1037,6 +1037,8 @@ fq_status fq_grouped_gated_bwd(const uint16_t *daq, const uint16_t *x, int32_t x
   (void)ws_bytes;
   FQ_TRY(check_product(x, x_rows, perm, topk, R_max, seg, s, true, 2, dh));
   FQ_CHECK_ARG(R_max == 0 || daq, "daq is NULL");
+  // a wave's 64 rows of dA lie within 32-bit offsets of their first
+  FQ_CHECK_SUPPORTED(s.N / 2 <= (1 << 25), "the gated backward takes F <= 2^25 (F=%d)", s.N / 2);
   FQ_CHECK_ARG((!daq || aligned16(daq)) && (!aqo || aligned16(aqo)) && w_fq && aligned16(w_fq),
                "w_fq must be non-NULL, bf16 tensors 16-byte aligned");
   FQ_TRY(check_act_q(aq, s.N / 2));

@@ -209,3 +209,12 @@ def test_norms_without_rows(pkg):  # noqa: F811
     for kw in (rows, dict(rows, w_post=None), dict(rows, w_pre=None)):
         assert call(pkg, "fq_norm_residual_bwd", norm_bwd(**kw))[0] == 0, kw
     assert call(pkg, "fq_norm_residual_fwd", norm_fwd(T=0, H=24))[0] == INVALID
+
+
+@host_only
+def test_gated_backward_refuses_columns_past_its_offsets(pkg):  # noqa: F811
+    """64 rows of dA are reached by 32-bit offsets: 128 F bytes, up to 2^32. (What passes
+    the checks fails at the launch, without a device.)"""
+    for F, bwd, fwd in ((1 << 25, 4, 4), ((1 << 25) + 16, UNSUPPORTED, 4)):
+        assert call(pkg, "fq_grouped_gated_bwd", gated_args(pkg, True, shape=(1, 2 * F, 16)))[0] == bwd
+        assert call(pkg, "fq_grouped_gated_fwd", gated_args(pkg, False, shape=(1, 2 * F, 16)))[0] == fwd
