@@ -583,9 +583,10 @@ fq_status fq_swiglu_bwd_ckpt(const uint16_t *daq_bf16, const uint8_t *codes, con
  *   fq_moe_permute gives it, x_rows = T). w: FQ_FMT_INT8 codes [E, N, K] as exported, group = K
  *   (scale [E, N]) or FQ_GROUP_TENSOR (scale [E]); the other fields unused.
  *   Rows from seg_offsets[E] on are left untouched.
- * K and N (gated: F) multiples of 16, K <= 131071, E <= 1024; an expert's codes,
- * and with perm the token rows, below 4 GiB; rows * K < 2^35 for the codes. codes,
- * x_codes, y and a 16-byte aligned, scales 4-byte. Outputs must not overlap inputs.
+ * K and N (gated: F) multiples of 16, K <= 131071, E <= 1024, R_max < 2^31 - 1024; an
+ * expert's codes, and with perm the token rows, below 4 GiB; rows * K < 2^35 for the
+ * codes. codes, x_codes, y and a 16-byte aligned, scales 4-byte. Outputs must not
+ * overlap inputs.
  * Workspace: fq_workspace_bytes(FQ_OP_GEMM_INT8, shape, R_max, 0), for the gated
  * product FQ_OP_GATED (0 bytes: ws may be NULL).
  * ---------------------------------------------------------------------- */
@@ -616,10 +617,10 @@ fq_status fq_grouped_gated_int8(const uint8_t *x_codes, const float *x_scale, in
  * output, or the raw weights). x_bf16 [x_rows, H] already fake-quantized, read
  * through perm / topk or (perm NULL) by routed row, as for the int8 products.
  * Rows from seg_offsets[E] on are left untouched. H, F % 16 == 0, H <= 2^20, F <= 2^25
- * in the backward, E <= 1024; an expert's matrix, and with perm the token rows, below 4 GiB. Outputs
- * must not overlap inputs or each other. The order of the sums, and with it the bits,
- * is fixed for a given R_max, shape and device (calls of another R_max may take tiles
- * of another size).
+ * in the backward, E <= 1024, R_max < 2^31 - 1024; an expert's matrix, and with perm the
+ * token rows, below 4 GiB. Outputs must not overlap inputs or each other. The order of the
+ * sums, and with it the bits, is fixed for a given R_max, shape and device (calls of
+ * another R_max may take tiles of another size).
  * Workspace: fq_workspace_bytes(FQ_OP_GATED, shape, R_max, 0) (0 bytes: may be NULL).
  * ---------------------------------------------------------------------- */
 fq_status fq_grouped_gated_fwd(const uint16_t *x_bf16, int32_t x_rows, const int32_t *perm,

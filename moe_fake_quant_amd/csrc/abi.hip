@@ -233,6 +233,8 @@ fq_status check_product(const void *x, int64_t x_rows, const int32_t *perm, int3
                         const void *out) {
   FQ_TRY(check_shape(s));
   FQ_CHECK_ARG(R_max >= 0 && x_rows >= 0, "R_max < 0 or x_rows < 0");
+  // rows are rounded up to whole tiles, and to whole experts, in int32
+  FQ_CHECK_SUPPORTED(R_max <= INT32_MAX - 1024, "R_max up to 2^31 - 1025 (R_max=%d)", R_max);
   FQ_CHECK_ARG(seg != nullptr, "seg_offsets is NULL");
   FQ_CHECK_ARG(R_max == 0 || (x && out), "NULL pointer");
   FQ_CHECK_ARG(!perm || topk > 0, "perm needs topk > 0 (topk=%d)", topk);

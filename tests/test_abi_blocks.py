@@ -218,3 +218,16 @@ def test_gated_backward_refuses_columns_past_its_offsets(pkg):  # noqa: F811
     for F, bwd, fwd in ((1 << 25, 4, 4), ((1 << 25) + 16, UNSUPPORTED, 4)):
         assert call(pkg, "fq_grouped_gated_bwd", gated_args(pkg, True, shape=(1, 2 * F, 16)))[0] == bwd
         assert call(pkg, "fq_grouped_gated_fwd", gated_args(pkg, False, shape=(1, 2 * F, 16)))[0] == fwd
+
+
+@host_only
+def test_products_refuse_row_counts_at_the_end_of_int32(pkg):  # noqa: F811
+    """Row counts are rounded up to tiles and experts in int32. (What passes the checks
+    fails at the launch, without a device.)"""
+    top = (1 << 31) - 1
+    for R, want in ((top - 1024, 4), (top - 1023, UNSUPPORTED), (top, UNSUPPORTED)):
+        kw = dict(R=R, rows=R, shape=(2, 32, 16))
+        for fn in ("fq_grouped_gemm_int8", "fq_grouped_gated_int8"):
+            assert call(pkg, fn, int8_args(pkg, w=stored(pkg, group=16), **kw))[0] == want, (fn, R)
+        assert call(pkg, "fq_grouped_gated_fwd", gated_args(pkg, False, **kw))[0] == want, R
+        assert call(pkg, "fq_grouped_gated_bwd", gated_args(pkg, True, **kw))[0] == want, R
