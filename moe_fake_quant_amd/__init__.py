@@ -425,7 +425,7 @@ def fq_topk_kl(student, teacher, T, V, K, reverse, valid, topk_idx, grad, loss_t
 
 
 # The calls below are marshalled natively (bind/bind.cpp): contiguous device tensors
-# on the current device, or None; shape (E, N, K).
+# on the current device, of the C type's elements, or None; shape (E, N, K).
 
 def fq_quantize_tokens(x, rows, K, n_rows, codes, scale):
     _check(_b.fq_quantize_tokens(x, rows, K, n_rows, codes, scale))

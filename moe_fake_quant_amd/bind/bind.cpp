@@ -5,9 +5,9 @@
 //
 // Every function takes the arguments of its C entry point without the stream and
 // with (ws, ws_bytes) as one tensor or None, positionally, and returns the status.
-// Tensors must be contiguous device tensors on the current device, of elements of the
-// C type's size; a shape is a
-// tuple (E, N, K), weights are StoredW, activation quantizers ActQ or None.
+// Tensors must be contiguous device tensors on the current device, of the C type's
+// elements (uint16_t: bf16, or 16-bit integers as raw storage); a shape is a tuple
+// (E, N, K), weights are StoredW, activation quantizers ActQ or None.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -15,11 +15,35 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <type_traits>
+
 #include "fq.h"
 
 namespace {
 
 struct Error {};  // a Python exception is set
+
+// What a pointer of fq.h may be given as: a float16 or an int32 of the right size would
+// only give wrong numbers.
+template <class T>
+constexpr const char *kWanted = "";
+template <>
+constexpr const char *kWanted<uint8_t> = "8-bit";
+template <>
+constexpr const char *kWanted<uint16_t> = "bfloat16";
+template <>
+constexpr const char *kWanted<int32_t> = "int32";
+template <>
+constexpr const char *kWanted<float> = "float32";
+template <class T>
+bool holds(const at::Tensor &t) {
+  const at::ScalarType s = t.scalar_type();
+  if (std::is_same<T, uint8_t>::value) return t.element_size() == 1 && s != at::kBool;
+  if (std::is_same<T, uint16_t>::value)
+    return s == at::kBFloat16 || s == at::kShort || s == at::kUInt16;
+  if (std::is_same<T, int32_t>::value) return s == at::kInt || s == at::kUInt32;
+  return s == at::kFloat;
+}
 
 PyObject *n_fmt, *n_group, *n_codes, *n_scale;
 
@@ -35,7 +59,7 @@ class Args {
   }
   template <class T>
   T *ptr() {
-    return static_cast<T *>(tensor(*a_++, sizeof(T)));
+    return tensor<T>(*a_++);
   }
   int32_t i32() {
     const long v = PyLong_AsLong(*a_++);
@@ -73,8 +97,8 @@ class Args {
     fq_stored_w r{};
     r.fmt = (int32_t)number(w, n_fmt);
     r.group = (int32_t)number(w, n_group);
-    r.codes = field(w, n_codes, 1);
-    r.scale = static_cast<const float *>(field(w, n_scale, 4));
+    r.codes = field<uint8_t>(w, n_codes);
+    r.scale = field<float>(w, n_scale);
     return r;
   }
   // an ActQ or None
@@ -82,13 +106,13 @@ class Args {
     PyObject *a = *a_++;
     if (a == Py_None) return nullptr;
     q.fmt = (int32_t)number(a, n_fmt);
-    q.scale = static_cast<const float *>(field(a, n_scale, 4));
+    q.scale = field<float>(a, n_scale);
     return &q;
   }
   // a workspace: pointer and size
   void *ws(size_t &bytes) {
     PyObject *o = *a_++;
-    void *p = tensor(o, 0);
+    void *p = data(o);
     bytes = p ? THPVariable_Unpack(o).nbytes() : 0;
     return p;
   }
@@ -98,8 +122,17 @@ class Args {
   PyObject *const *a_;
   c10::DeviceIndex dev_;
 
-  // elem: bytes of an element (0: any)
-  void *tensor(PyObject *o, size_t elem) {
+  template <class T>
+  T *tensor(PyObject *o) {
+    void *p = data(o);
+    if (o != Py_None && !holds<T>(THPVariable_Unpack(o))) {
+      PyErr_Format(PyExc_ValueError, "a tensor of %s elements is wanted, not of %s", kWanted<T>,
+                   c10::toString(THPVariable_Unpack(o).scalar_type()));
+      throw Error{};
+    }
+    return static_cast<T *>(p);
+  }
+  void *data(PyObject *o) {
     if (o == Py_None) return nullptr;
     if (!THPVariable_Check(o)) {
       PyErr_Format(PyExc_TypeError, "a tensor or None is wanted, not %s", Py_TYPE(o)->tp_name);
@@ -119,11 +152,6 @@ class Args {
       PyErr_SetString(PyExc_ValueError, "libfq takes contiguous tensors");
       throw Error{};
     }
-    if (elem && t.element_size() != elem) {
-      PyErr_Format(PyExc_ValueError, "a tensor of %zu-byte elements is wanted, not of %zu bytes", elem,
-                   (size_t)t.element_size());
-      throw Error{};
-    }
     return t.data_ptr();
   }
   PyObject *get(PyObject *o, PyObject *name) {
@@ -138,14 +166,15 @@ class Args {
     if (r == -1 && PyErr_Occurred()) throw Error{};
     return r;
   }
-  void *field(PyObject *o, PyObject *name, size_t elem) {
+  template <class T>
+  T *field(PyObject *o, PyObject *name) {
     PyObject *v = get(o, name);
     // the object keeps its tensor alive; v is only this look at it
     struct Drop {
       PyObject *p;
       ~Drop() { Py_DECREF(p); }
     } drop{v};
-    return tensor(v, elem);
+    return tensor<T>(v);
   }
 };
 
