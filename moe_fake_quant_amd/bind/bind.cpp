@@ -178,6 +178,13 @@ class Args {
   }
 };
 
+// The C call itself without the interpreter lock: a launch may wait for room in the queue,
+// and other threads (a host function of the same stream among them) go on meanwhile.
+struct Unlocked {
+  PyThreadState *t = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(t); }
+};
+
 template <class F>
 PyObject *guarded(F f) {
   try {
@@ -203,7 +210,9 @@ FN(quantize_tokens) {
     const auto *n_rows = a.ptr<int32_t>();
     auto *codes = a.ptr<uint8_t>();
     auto *scale = a.ptr<float>();
-    return fq_quantize_tokens(x, rows, K, n_rows, codes, scale, a.stream());
+    const fq_stream st = a.stream();
+    Unlocked u;
+    return fq_quantize_tokens(x, rows, K, n_rows, codes, scale, st);
   });
 }
 
@@ -222,7 +231,9 @@ PyObject *int8_call(const char *fn, Call call, PyObject *const *argv, Py_ssize_t
     auto *out = a.ptr<uint16_t>();
     size_t bytes;
     void *ws = a.ws(bytes);
-    return call(xc, sx, x_rows, perm, topk, R, seg, s, &w, out, ws, bytes, a.stream());
+    const fq_stream st = a.stream();
+    Unlocked u;
+    return call(xc, sx, x_rows, perm, topk, R, seg, s, &w, out, ws, bytes, st);
   });
 }
 FN(grouped_gemm_int8) { return int8_call("fq_grouped_gemm_int8", fq_grouped_gemm_int8, argv, n); }
@@ -243,7 +254,9 @@ FN(grouped_gated_fwd) {
     auto *out = a.ptr<uint16_t>();
     size_t bytes;
     void *ws = a.ws(bytes);
-    return fq_grouped_gated_fwd(x, x_rows, perm, topk, R, seg, s, w, aq, out, ws, bytes, a.stream());
+    const fq_stream st = a.stream();
+    Unlocked u;
+    return fq_grouped_gated_fwd(x, x_rows, perm, topk, R, seg, s, w, aq, out, ws, bytes, st);
   });
 }
 
@@ -264,8 +277,9 @@ FN(grouped_gated_bwd) {
     auto *aqo = a.ptr<uint16_t>();
     size_t bytes;
     void *ws = a.ws(bytes);
-    return fq_grouped_gated_bwd(daq, x, x_rows, perm, topk, R, seg, s, w, aq, dh, aqo, ws, bytes,
-                                a.stream());
+    const fq_stream st = a.stream();
+    Unlocked u;
+    return fq_grouped_gated_bwd(daq, x, x_rows, perm, topk, R, seg, s, w, aq, dh, aqo, ws, bytes, st);
   });
 }
 
@@ -284,8 +298,9 @@ FN(norm_residual_fwd) {
     auto *nn = a.ptr<uint16_t>();
     auto *codes = a.ptr<uint8_t>();
     auto *scale = a.ptr<float>();
-    return fq_norm_residual_fwd(x, b, gate, alpha, w_post, w_pre, eps, T, H, y, nn, codes, scale,
-                                a.stream());
+    const fq_stream st = a.stream();
+    Unlocked u;
+    return fq_norm_residual_fwd(x, b, gate, alpha, w_post, w_pre, eps, T, H, y, nn, codes, scale, st);
   });
 }
 
@@ -309,8 +324,10 @@ FN(norm_residual_bwd) {
     auto *dw_pre = a.ptr<float>();
     size_t bytes;
     void *ws = a.ws(bytes);
+    const fq_stream st = a.stream();
+    Unlocked u;
     return fq_norm_residual_bwd(dy, dn, y, b, gate, alpha, w_post, w_pre, eps, T, H, dx, db, dgate,
-                                dw_post, dw_pre, ws, bytes, a.stream());
+                                dw_post, dw_pre, ws, bytes, st);
   });
 }
 

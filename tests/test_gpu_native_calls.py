@@ -1,4 +1,8 @@
 """The native marshalling of the int8, gated and norm calls: what it takes and refuses."""
+import sys
+import threading
+import time
+
 import pytest
 import torch
 
@@ -46,3 +50,25 @@ def test_elements_of_another_type_are_refused():
     # raw storage and signed codes are the same bytes
     F.fq_quantize_tokens(x.view(torch.int16), 4, 32, None, codes.view(torch.int8), s)
     F.fq_grouped_gemm_int8(codes.view(torch.int8), s, 4, perm, 1, 4, seg, (1, 32, 32), st, y.view(torch.int16))
+
+
+def test_calls_release_the_interpreter_lock():
+    """A thread that waits for the lock gets it during a call: the interpreter itself would
+    not pass it on within 1000 s here."""
+    woken, old = threading.Event(), sys.getswitchinterval()
+
+    def waiter():
+        time.sleep(0.1)       # without the lock; then waits for it
+        woken.set()
+
+    t = threading.Thread(target=waiter)
+    try:
+        sys.setswitchinterval(1000.0)
+        t.start()
+        end = time.monotonic() + 5.0
+        while not woken.is_set() and time.monotonic() < end:
+            F.fq_quantize_tokens(None, 0, 16, None, None, None)
+        assert woken.is_set()
+    finally:
+        sys.setswitchinterval(old)
+        t.join()
