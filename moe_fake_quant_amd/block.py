@@ -29,6 +29,11 @@ def _in(t: torch.Tensor, *buffers: torch.Tensor) -> bool:
     return any(_at(t) == _at(b) for b in buffers)
 
 
+def _shifted(t: torch.Tensor, buffer: torch.Tensor) -> bool:
+    """Rows of the buffer, but not its first ones: written in place, each would land on another."""
+    return _in(t, buffer) and t.data_ptr() != buffer.data_ptr()
+
+
 class MoEFakeQuantBlock:
     def __init__(self, layer: MoEFakeQuantLayer, w_pre: torch.Tensor,
                  w_post: Optional[torch.Tensor] = None, alpha: float = 1.0, eps: float = 1e-6,
@@ -88,13 +93,13 @@ class MoEFakeQuantBlock:
 
     def backward(self, probs: torch.Tensor, dy: torch.Tensor):
         """dx, and the layer's scale gradients (ds_gu, ds_d); dgate [T], dw_pre and dw_post
-        are the block's where they exist."""
+        are the block's where they exist. dy may be the block's own dx, from its first row on."""
         if self.x is None:
             raise ValueError("backward needs a forward")
         T, H = self.x.shape[0], self.layer.H
         if dy.shape != (T, H) or dy.dtype != torch.bfloat16:
             raise ValueError(f"dy must be bf16 [{T}, {H}]")
-        if _in(dy, self.db) or _at(dy) in self.layer._scratch_at:
+        if _in(dy, self.db) or _shifted(dy, self.dx) or _at(dy) in self.layer._scratch_at:
             raise ValueError("dy lies in a buffer that the layer's backward overwrites")
         fq_norm_residual_bwd(dy, None, None, self.b[:T], self.gate, self.alpha, self.w_post, None,
                              self.eps, T, H, None, self.db[:T],
@@ -107,11 +112,12 @@ class MoEFakeQuantBlock:
     def forward_int8(self, x: torch.Tensor, expert_ids: torch.Tensor, probs: torch.Tensor,
                      gate: Optional[torch.Tensor] = None) -> torch.Tensor:
         """y over the layer's exported int8 stacks: the norm's output goes to the products
-        as codes with a scale a token and is never stored in bf16."""
+        as codes with a scale a token and is never stored in bf16. x may be the block's own
+        y, from its first row on."""
         T = self._check(x, gate)
         self.layer._check_int8()
-        if _in(x, self.layer.i8["out"]):
-            raise ValueError("x lies in the buffer that the layer's output overwrites")
+        if _in(x, *(self.layer.i8[k] for k in ("a", "o", "out"))) or _shifted(x, self.y):
+            raise ValueError("x lies in a buffer that the layer's steps overwrite, or in other rows of y")
         codes, scale = self.layer.i8["x_codes"], self.layer.i8["x_scale"]
         fq_norm_residual_fwd(x, None, None, 1.0, None, self.w_pre, self.eps, T, self.layer.H, None, None,
                              codes, scale)

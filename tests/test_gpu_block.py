@@ -349,3 +349,25 @@ def test_block_without_tokens(post, gated, mode):
     assert dx.shape == (0, layer.H) and not ds_gu.any() and not ds_d.any() and not blk.dw_pre.any()
     assert not post or not blk.dw_post.any()
     assert blk.forward_int8(x[:0], ids[:0], p[:0], gate).shape == (0, layer.H)
+
+
+def test_block_refuses_other_rows_of_the_buffers_it_writes():
+    """x within y, or dy within dx, at another row: written in place, a row would overwrite
+    one that is still to be read. The same for the int8 layer's inner buffers as x."""
+    layer, x, ids, p, dy = make(O.FMT_INT8, O.FMT_INT8, None)
+    T = x.shape[0]
+    blk = block_of(layer)
+    layer.quantize_weights()
+    layer.export()
+    blk.forward_int8(x, ids, p)
+    n = T - 3
+    for bad in (blk.y[3:T], layer.i8["o"][:n], layer.i8["o"][5:5 + n]):
+        with pytest.raises(ValueError):
+            blk.forward_int8(bad, ids[:n], p[:n])
+    blk.forward(x[:n], ids[:n], p[:n])
+    with pytest.raises(ValueError):
+        blk.backward(p[:n], blk.dx[3:T])
+    # fewer rows from the first one on are in place row by row
+    blk.dx[:n].copy_(dy[:n])
+    got = bits(blk.backward(p[:n], blk.dx[:n])[0])
+    assert same(got, bits(blk.backward(p[:n], dy[:n])[0]))
