@@ -68,6 +68,8 @@ class MoEFakeQuantBlock:
             raise ValueError(f"x must be bf16 [T <= {self.layer.T_max}, {self.layer.H}]")
         if gate is not None and (gate.shape != (T,) or gate.dtype != torch.float32):
             raise ValueError(f"gate must be float32 [{T}]")
+        if gate is not None and _in(gate, self.dgate):
+            raise ValueError("gate lies in the block's dgate, which the backward overwrites")
         return T
 
     def _join(self, x, b, gate, T):

@@ -371,3 +371,17 @@ def test_block_refuses_other_rows_of_the_buffers_it_writes():
     blk.dx[:n].copy_(dy[:n])
     got = bits(blk.backward(p[:n], blk.dx[:n])[0])
     assert same(got, bits(blk.backward(p[:n], dy[:n])[0]))
+
+
+def test_block_refuses_its_gate_gradient_as_the_gate():
+    """The gate is kept by reference: the first backward would overwrite it."""
+    layer, x, ids, p, dy = make(O.FMT_FP8, O.FMT_FP8, None)
+    blk = block_of(layer)
+    layer.quantize_weights()
+    blk.dgate.fill_(0.5)
+    T = x.shape[0]
+    with pytest.raises(ValueError):
+        blk.forward(x, ids, p, blk.dgate[:T])
+    blk.forward(x, ids, p, blk.dgate[:T].clone())
+    first = bits(blk.backward(p, dy)[0])
+    assert same(bits(blk.backward(p, dy)[0]), first)
