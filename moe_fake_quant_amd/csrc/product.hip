@@ -154,37 +154,58 @@ __global__ __launch_bounds__(NW * 64) void k_rows_product(ProdArgs a) {
 // would give. us of one call on 256 CUs, int8 / gated int8 / gated bf16, its backward:
 //   rows an expert      few rows          64 x 64             128 x 128           256 x 256
 //   one [4096 x 4096]
-//     16                8 / 9 / 14, 15    11 / 11 / 19, 19    16 / 16 / 29, 29    36 / 37 / 66, 68
-//     64                13 / 16 / 26, 27  11 / 12 / 20, 21    17 / 17 / 30, 32    36 / 37 / 66, 70
+//     16                8 / 9 / 15, 15    12 / 12 / 20, 20    17 / 17 / 30, 31    36 / 37 / 66, 69
+//     32                10 / 11 / 19, 19  12 / 12 / 20, 20    17 / 17 / 30, 31    36 / 37 / 67, 70
+//     48                13 / 15 / 26, 26  12 / 12 / 20, 20    17 / 17 / 31, 32    36 / 37 / 67, 70
+//     64                14 / 16 / 26, 27  12 / 12 / 21, 21    17 / 17 / 31, 32    36 / 37 / 67, 71
+//     128               24 / 16 / 27, 28  12 / 12 / 21, 21    18 / 18 / 36, 37    40 / 41 / 75, 79
 //     512               87 / 55 / 94, 97  17 / 17 / 30, 31    19 / 19 / 33, 36    44 / 46 / 81, 86
 //     1024                                29 / 29 / 55, 57    22 / 21 / 37, 40    44 / 46 / 82, 86
 //     2048                                55 / 54 / 107, 117  37 / 36 / 66, 72    50 / 49 / 83, 86
+//   rows of one expert over short contractions, where the few-row form's stream is over soon
+//     [2048 x 2048] 64  7.8 / 9.4 / 15, 15    7.9 / 7.9 / 12, 12
+//     [1024 x 1024] 64  4.9 / 6.0 / 8.5, 8.9  5.6 / 5.6 / 7.8, 8.0
+//     8 of [256 x 512]  4.0 / 4.9 / 5.9, 6.4  5.4 / 5.4 / 6.2, 6.7  (64 rows each)
 //   128 of [1536 x 2048]
 //     16            121 / 131 / 211, 227  80 / 79 / 146, 155  86 / 83 / 155, 158  90 / 90 / 162, 170
 //     64                                  95 / 92 / 167, 178  94 / 89 / 164, 180  93 / 92 / 202, 214
 //     128                                 143 / 140 / 249, 259  120 / 111 / 201, 233  104 / 98 / 200, 217
 //     256                                 250 / 245 / 416, 443  190 / 175 / 273, 306  132 / 126 / 215, 237
 //   64 of [2048 x 768], 1024 rows         298 / 279 / 411, 503  211 / 179 / 281, 366  154 / 143 / 216, 270
+// The rows that are really there are known on the device alone. 32 of [1536 x 2048] with
+// room for 512 rows an expert, which the rule gives tiles of 256, with fewer live:
+//     256                                 64 / 62 / 106, 114  47 / 46 / 79, 89    37 / 41 / 64, 68
+//     128                                 38 / 39 / 66, 68    33 / 32 / 56, 59    37 / 35 / 57, 60
+//     64                                  26 / 26 / 51, 50    29 / 29 / 52, 54    34 / 34 / 56, 59
 enum Form { kRows, kMid64, kMid128, kTile256 };
 
-static Form pick_form(const ProdArgs &a, int kind, int R_max) {
-  const int64_t cus = device_cus(), per = (R_max + a.E - 1) / a.E;
+static Form pick_form(int kind, int E, int C, uint32_t KB, int R_max) {
+  const int64_t cus = device_cus(), per = ((int64_t)R_max + E - 1) / E;
   auto units = [&](int64_t tile) {
     const int64_t cols = kind == PLAIN ? tile : tile / 2;
-    return (a.C + cols - 1) / cols * a.E * ((per + tile - 1) / tile);
+    return (C + cols - 1) / cols * E * ((per + tile - 1) / tile);
   };
   // blocks of 16 columns and up to 64 rows: two rounds of them at most for up to 32 rows
-  // an expert, one beyond
-  const int64_t blocks = (int64_t)(a.C / 16) * a.E * ((per + 63) / 64);
-  if (blocks <= (per <= 32 ? 2 * cus : cus)) return kRows;
+  // an expert; beyond, one round, and only over rows of 2 KB (gated: 1 KB)
+  const int64_t blocks = (int64_t)(C / 16) * E * ((per + 63) / 64);
+  const bool few = per <= 32 ? blocks <= 2 * cus
+                             : blocks <= cus && KB <= (kind == PLAIN ? 2048u : 1024u);
+  if (few) return kRows;
   if (per > 64 && units(256) >= cus) return kTile256;
   if (per > 64 && units(128) * 4 >= cus * 3) return kMid128;
   return kMid64;
 }
 
+// Not part of fq.h: the form (0 to 3) that a call takes on the current device, for the
+// tests that aim at each of them. kind: 0 plain, 1 gated, 2 its backward.
+extern "C" int32_t fq_internal_product_form(int32_t kind, int32_t E, int32_t columns, int32_t row_bytes,
+                                            int32_t R_max) {
+  return pick_form(kind, E, columns, (uint32_t)row_bytes, R_max);
+}
+
 template <int KIND, bool I8>
 static void launch_product(const ProdArgs &a, int R_max, hipStream_t st) {
-  const Form form = pick_form(a, KIND, R_max);
+  const Form form = pick_form(KIND, a.E, a.C, a.KB, R_max);
   if (form == kTile256) return launch_tile_product(a, KIND, I8, R_max, st);
   if (form != kRows) return launch_mid_product(a, KIND, I8, form == kMid64 ? 64 : 128, R_max, st);
   const int per = (R_max + a.E - 1) / a.E;
