@@ -88,9 +88,10 @@ def test_rows_of_very_large_values(H, size):
 
 
 @pytest.mark.parametrize("H", [48, 2064])
-@pytest.mark.parametrize("eps", [2.0 ** -126, 2.0 ** -90])
+@pytest.mark.parametrize("eps", [2.0 ** -149, 2.0 ** -126, 2.0 ** -90])
 def test_the_smallest_eps_and_rows_of_zeros(H, eps):
-    """A row of zeros has the root 2^63 (2^45): dx = dy + 2^63 dn w_pre there, and no NaN."""
+    """A row of zeros has the root eps^-1/2 (up to 2^74.5): dx = dy + dn w_pre eps^-1/2
+    there, and no NaN."""
     print(f"[norm eps] H={H} eps={eps}", flush=True)
     T, rng = 6, np.random.default_rng(H)
     y, b, dy = (normal_bits(rng, T, H) for _ in range(3))
@@ -98,3 +99,32 @@ def test_the_smallest_eps_and_rows_of_zeros(H, eps):
     y[1] = y[4] = b[2] = b[4] = 0
     args = (dy, dn, y, b, rng.standard_normal(T).astype(np.float32), 0.5, _weights(rng, H), _weights(rng, H), eps)
     _check(_run(*args), *args)
+
+
+# rows of a wave (4096 in flight), of four waves (1024) and of eight and four waves (512): each
+# block takes its second and its third row
+@pytest.mark.parametrize("T,H", [(9001, 48), (8200, 512), (2500, 528), (2100, 2048), (1300, 2064), (1100, 4112),
+                                 (1030, 8208)])
+@pytest.mark.parametrize("post", [True, False])
+def test_more_rows_than_blocks(T, H, post):
+    print(f"[norm rows] T={T} H={H} post={post}", flush=True)
+    rng = np.random.default_rng(T)
+    y, b, dy, dn = (normal_bits(rng, T, H) for _ in range(4))
+    y[::7], b[::11] = 0, 0
+    gate = rng.standard_normal(T).astype(np.float32)
+    args = (dy, dn, y, b, gate, 0.5, _weights(rng, H), _weights(rng, H), 1e-6)
+    got = _run(*args)
+    _check(got, *args)
+    # and without the weights' sums, a block to every row
+    frozen = _run(*args, frozen=True)
+    assert all(np.array_equal(frozen[k], got[k]) for k in frozen)
+    if post:
+        return
+    # without b every row ends at its first sum: one barrier a row
+    out = dict(dx=torch.full((T, H), FILL, dtype=torch.bfloat16, device="cuda"),
+               dw_pre=torch.full((H,), FILL, device="cuda"))
+    ws = torch.empty(F.fq_workspace_bytes(F.FQ_OP_NORM, (1, T, H), 0, 0), dtype=torch.uint8, device="cuda")
+    F.fq_norm_residual_bwd(dev_bf16(dy), dev_bf16(dn), dev_bf16(y), None, None, 1.0, None, dev_bf16(args[7]),
+                           1e-6, T, H, **out, ws=ws)
+    assert np.array_equal(bf16_vals(host_bits(out["dx"])), got["dx"])
+    assert np.array_equal(out["dw_pre"].cpu().numpy().astype(np.float64), got["dw_pre"])
