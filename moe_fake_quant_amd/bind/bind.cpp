@@ -1,7 +1,7 @@
 // Native marshalling of the calls that a decoding loop makes one after the other:
-// torch tensors -> the C ABI of fq.h, on the current device's current stream. A call
-// with eight tensors takes under 1 us here and 8 us through ctypes, more than the
-// small kernels themselves.
+// torch tensors -> the C ABI of fq.h, on the current device's current stream. A call with
+// its launch takes 3.5 to 4 us of host time here (0.2 us where nothing is enqueued) and 8
+// through ctypes, more than the small kernels themselves.
 //
 // Every function takes the arguments of its C entry point without the stream and
 // with (ws, ws_bytes) as one tensor or None, positionally, and returns the status.

@@ -107,7 +107,7 @@ void launch_int8_product(const uint8_t *xc, const float *sx, const int32_t *perm
 void launch_gated(const uint16_t *daq, const uint16_t *x, const int32_t *perm, int topk, int R_max,
                   const int32_t *seg, fq_shape s, const uint16_t *w, int afmt, const float *ascale,
                   uint16_t *out, uint16_t *aq, hipStream_t st);
-// norms around a block; rows up to kNormWaveRow lie in one wave, up to kNormMaxRow in four
+// norms around a block; rows up to kNormWaveRow lie in one wave, up to kNormMaxRow in four or eight
 constexpr int kNormWaveRow = 512, kNormMaxRow = 16384;
 size_t norm_ws_bytes(int T, int H);
 void launch_norm_fwd(const uint16_t *x, const uint16_t *b, const float *gate, float alpha,

@@ -9,9 +9,9 @@
 // last step (scales, SwiGLU, its gradient, fake-quant, stores) works on 8 columns of
 // a row a thread, as in product.hip.
 //
-// Measured, the kernel alone: int8 over 2048 rows of [4096 x 4096] 37.6 us (1.83 POP/s,
+// Measured, the kernel alone: int8 over 2048 rows of [4096 x 4096] 38.7 us (1.77 POP/s,
 // the matrix unit busy 38 % of the time; a large plain int8 product reaches 2.05); 333
-// rows on five experts of [1040 x 368] 6.2 us, where the first stage's wait, the other
+// rows on five experts of [1040 x 368] 6.3 us, where the first stage's wait, the other
 // two stages and the epilogue stand one after the other.
 //
 // Gated: of the weight rows of each wave the first half are gate rows f, the second

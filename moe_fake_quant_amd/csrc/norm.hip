@@ -16,9 +16,11 @@
 //
 // All passes are HBM streams: a row stays in registers between its sums and its
 // outputs, so every tensor is read once and written once. Measured with a device copy
-// at 5.2 TB/s: the forward over 16384 x 2048 52 us (5.1 TB/s), the backward with every
-// gradient over 8191 x 2048 54 us (3.7 TB/s; about 40 vector instructions an element, and
-// the weights' sums leave as block sums that a second kernel adds in block order, 5 us).
+// at 5.2 TB/s: the forward over 16384 x 2048 52 us (5.1 TB/s); the backward over 8191 x
+// 2048 44 us without the weights' gradients (4.6 TB/s), with them 49 us (4.1 TB/s, without
+// the block sums, 17 MB) and 5 us for the kernel that adds those in block order. The vector
+// units are busy 35 to 41 % of the time (46 instructions an element): the backward waits
+// for HBM, since a block's next row is asked for after the row before has been stored.
 #include <type_traits>
 
 #include "internal.hpp"
@@ -290,8 +292,8 @@ __global__ __launch_bounds__(1024) void k_norm_dw(const float *__restrict__ part
 }
 
 // x [rows, K] -> codes [rows, K] with a scale for each row; rows too long for the
-// registers are read twice. An HBM stream: 131072 rows of 768 in 55 us (5.5 TB/s
-// with the codes), 2048 rows of 4096 in 6.6.
+// registers are read twice. An HBM stream: 131072 rows of 768 in 59 us (5.1 TB/s
+// with the codes; the fastest 54), 2048 rows of 4096 in 6.9.
 template <int WPR, int VPT>
 __global__ __launch_bounds__(kRowThreads<WPR>) void k_quantize_tokens(const bf16x8_t *__restrict__ x,
                                                                  int rows, int nv,

@@ -1,5 +1,5 @@
 // Arguments of the int8 and gated products, shared by the kernels for few rows
-// (product.hip) and the tiled ones (tile_product.hip).
+// (product.hip), a middling number (mid_product.hip) and many (tile_product.hip).
 #pragma once
 
 #include "actq.hpp"

@@ -14,19 +14,29 @@
 // no exchange but the amax of an NVFP4 block between the lane halves, and h never
 // leaves the registers.
 //
-// A stage takes about 1.8 us, twice what its MFMAs need (the matrix unit is busy 46 to
-// 49 % of the time), for both types and also where all operands lie in L2; a tile has
-// 5 to 7 us around its stages (28 % busy for int8 with a contraction of 768). The
-// operands' way through L1 into LDS bounds it, not the LDS reads or the barriers: four
-// waves of 128 x 128, with two thirds of the LDS reads and half the barriers, took as
-// long a stage (and 10 to 20 % more in all, for a longer epilogue). Without its stores
-// the kernel takes 4 % (gated) to 20 % (int8, 768) less. Loads of a later stage issued
-// ahead into L2 made it 30 % slower; eighths of the experts starting at different
-// stages, 2 % slower at 512 and more rows an expert (at 128 rows of bf16 between 0 and 15
-// % faster, by the card); a higher wave priority for the multiplying group, flat.
-// Measured with 128 experts, the kernel alone: gated forward over 65536 rows, H 2048, F
-// 768, FP8 443 us (931 TFLOP/s); its backward over 131072 rows 860 us (959 TFLOP/s);
-// int8 over 131072 rows of [2048 x 768] 335 us (1.23 POP/s).
+// A stage takes about 1.8 us with every CU at work, twice what its MFMAs need (the matrix
+// unit is busy 46 to 49 % of the time), for both types and also where all operands lie in
+// L2; a tile has 5 to 7 us around its stages (28 % busy for int8 with a contraction of
+// 768). What bounds a stage is not settled:
+// - not the operands' bytes through L1 into LDS: 64 KB in 1.8 us are 9.3 TB/s over the
+//   chip, and the 128 x 128 form of mid_product.hip moves 13.9 TB/s that way;
+// - not the LDS reads or the barriers: four waves of 128 x 128, with two thirds of the
+//   reads and half the barriers, took as long a stage (and 10 to 20 % more in all, for a
+//   longer epilogue);
+// - more likely the chain of waits: with 32 CUs at work a stage still takes up to 1.4 us
+//   (512 rows of one int8 [4096 x 4096]: 44 us), and group A, which carries three quarters
+//   of a stage's loads, waits for all of them before it issues the next ones.
+// Without its stores the kernel takes 4 % (gated) to 20 % (int8, 768) less. Loads of a
+// later stage issued ahead into L2 made it 30 % slower; eighths of the experts starting at
+// different stages, 2 % slower at 512 and more rows an expert (at 128 rows of bf16 between
+// 0 and 15 % faster, by the card); a higher wave priority for the multiplying group, flat.
+// Measured with 128 experts, the kernel alone, fastest and average of 24 launches under the
+// trace: gated forward over 65536 rows, H 2048, F 768, FP8 444 and 522 us (929 and 790
+// TFLOP/s); its backward over 131072 rows 859 and 927 us (960, 890); int8 over 131072 rows
+// of [2048 x 768] 332 and 360 us (1.24 and 1.15 POP/s).
+//
+// The backward's epilogue needs a few registers more than there are under an activation
+// format: 2 go to scratch for INT8 and FP8, 28 for NVFP4, none inside the contraction loop.
 //
 // Rows and columns past the ends are clamped in the load addresses and not stored.
 // A contraction that ends inside a stage: the loading wave overwrites the chunks
