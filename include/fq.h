@@ -373,7 +373,8 @@ fq_status fq_grouped_gemm_bwd_scale(const uint16_t *dy_bf16, const uint16_t *x_b
  * never formed.
  *
  * fq_actfq: xq = FQ_a(x), row by row (NVFP4: 16-blocks along K).
- *   x, xq [rows, K] bf16, K % 16 == 0. aq NULL or FMT_NONE copies x.
+ *   x, xq [rows, K] bf16, K % 16 == 0, rows * K <= 3 * 2^33. aq NULL or
+ *   FMT_NONE copies x.
  * fq_grouped_gemm_fwd_tokens: fq_grouped_gemm_fwd with, for every routed
  *   row r < seg_offsets[E], x_bf16[r] = x_tok[perm[r] / topk].
  *   x_tok [T, K] is already fake-quantized, so the call takes no
@@ -427,7 +428,8 @@ fq_status fq_grouped_gemm_wgrad_tokens(const uint16_t *dy_bf16, const uint16_t *
  * fq_moe_combine_bwd: do[row_of[t,j]] = bf16(p[t,j] * dout[t]) for every
  *   routed slot; each dout row is read once.
  * fq_moe_unpermute_reduce: dx[t] = bf16(m_a(x[t]) * sum_j dxq[row_of[t,j]]).
- * All require H (resp. F) % 16 == 0 and T * H (resp. R_max * F) < 2^35.
+ * All require H (resp. F) % 16 == 0 and T * H (resp. R_max * F) < 2^35; the gather,
+ * fq_swiglu_actfq and fq_moe_combine_bwd at most 3 * 2^33.
  * T == 0 launches nothing (the token pointers may then be NULL).
  *
  * Learnable activation scale (fq_swiglu_bwd, fq_moe_unpermute_reduce): the

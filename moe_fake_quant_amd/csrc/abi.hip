@@ -29,6 +29,9 @@ fq_status hip_status(hipError_t e, const char *what) {
 namespace {
 
 constexpr size_t kAlign = 256;
+// Passes over vectors of 8 stride by up to 2^30 of them in 32 bits: the index of the next
+// one, which ends a thread's loop, stays in range for up to 3 * 2^30.
+constexpr int64_t kMaxVec8Elems = 3ll << 33;
 inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 struct Carver {
@@ -798,7 +801,7 @@ fq_status fq_actfq(const uint16_t *x, int32_t rows, int32_t K, const fq_act_q *a
   FQ_CHECK_ARG(rows >= 0 && K > 0 && K % 16 == 0, "bad sizes (rows=%d K=%d; K %% 16 == 0)", rows, K);
   FQ_CHECK_ARG(rows == 0 || (x && xq), "NULL pointer");
   FQ_CHECK_ARG((!x || aligned16(x)) && (!xq || aligned16(xq)), "bf16 tensors must be 16-byte aligned");
-  FQ_CHECK_ARG((long)rows * K < (1l << 35), "too many elements");
+  FQ_CHECK_ARG((long)rows * K <= kMaxVec8Elems, "too many elements");
   FQ_TRY(check_act_q(aq, K));
   launch_act_fq(x, (size_t)rows, K, nullptr, act_fmt(aq), aq ? aq->scale : nullptr, xq, S(stream));
   FQ_CHECK_LAUNCH("fq_actfq");
@@ -811,7 +814,7 @@ fq_status fq_moe_gather_actfq(const uint16_t *x, int32_t T, int32_t H, const int
   FQ_CHECK_ARG(H % 16 == 0, "H must be a multiple of 16");
   FQ_CHECK_ARG(T == 0 || (x && row_of && xq), "NULL pointer");
   FQ_CHECK_ARG((!x || aligned16(x)) && (!xq || aligned16(xq)), "bf16 tensors must be 16-byte aligned");
-  FQ_CHECK_ARG((long)T * H < (1l << 35), "too many elements");
+  FQ_CHECK_ARG((long)T * H <= kMaxVec8Elems, "too many elements");
   FQ_TRY(check_act_q(aq, H));
   launch_gather_actfq(x, T, H, row_of, topk, act_fmt(aq), aq ? aq->scale : nullptr, xq, S(stream));
   FQ_CHECK_LAUNCH("fq_moe_gather_actfq");
@@ -821,7 +824,7 @@ fq_status fq_moe_gather_actfq(const uint16_t *x, int32_t T, int32_t H, const int
 fq_status fq_swiglu_actfq(const uint16_t *h, int32_t R_max, const int32_t *n_rows, int32_t F,
                           const fq_act_q *aq, uint16_t *a, uint16_t *aqo, fq_stream stream) {
   FQ_CHECK_ARG(R_max >= 0 && F > 0 && F % 16 == 0, "bad sizes (F must be a multiple of 16)");
-  FQ_CHECK_ARG((long)R_max * F < (1l << 35), "too many elements");
+  FQ_CHECK_ARG((long)R_max * F <= kMaxVec8Elems, "too many elements");
   FQ_CHECK_ARG(n_rows && (R_max == 0 || (h && aqo)), "NULL pointer");
   FQ_CHECK_ARG((!h || aligned16(h)) && (!a || aligned16(a)) && (!aqo || aligned16(aqo)),
                "bf16 tensors must be 16-byte aligned");
@@ -861,7 +864,7 @@ fq_status fq_moe_combine(const uint16_t *o, const float *probs, const int32_t *r
 fq_status fq_moe_combine_bwd(const uint16_t *dout, const float *probs, const int32_t *row_of,
                              int32_t T, int32_t topk, int32_t H, uint16_t *dO, fq_stream stream) {
   FQ_CHECK_ARG(T >= 0 && topk > 0 && H > 0 && H % 16 == 0, "bad sizes (H must be a multiple of 16)");
-  FQ_CHECK_ARG((long)T * H < (1l << 35), "too many elements");
+  FQ_CHECK_ARG((long)T * H <= kMaxVec8Elems, "too many elements");
   FQ_CHECK_ARG(T == 0 || (dout && probs && row_of && dO), "NULL pointer");
   FQ_CHECK_ARG((!dout || aligned16(dout)) && (!dO || aligned16(dO)),
                "bf16 tensors must be 16-byte aligned");
