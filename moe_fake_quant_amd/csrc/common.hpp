@@ -83,6 +83,15 @@ __device__ __forceinline__ float warp_max(float v) {
 
 inline int ceil_div(long a, long b) { return (int)((a + b - 1) / b); }
 
+// A grid of any number of blocks of up to 512 threads: 2^32 or more threads along x lose
+// blocks without an error, so blocks beyond 2^22 go along y. The grid's last row may hold
+// more blocks than were asked for.
+inline dim3 block_grid(int blocks) {
+  constexpr int kX = 1 << 22;
+  return blocks <= kX ? dim3(blocks) : dim3(kX, ceil_div(blocks, kX));
+}
+__device__ __forceinline__ uint32_t block_of_grid() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Division of 32-bit unsigned numerators by a runtime divisor d >= 1 with a
 // multiply-high and a shift (round-up method, Hacker's Delight 10-9):
 // l = ceil(log2 d), M = floor(2^32 (2^l - d) / d) + 1, q = (mulhi(x, M) + x) >> l.

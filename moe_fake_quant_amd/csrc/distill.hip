@@ -345,8 +345,8 @@ __device__ __forceinline__ uint32_t wave_count(bool f) {
 // row is selected again by histograms (select_hist). Exact either way.
 template <bool REVERSE, int KM>
 __global__ __launch_bounds__(kKT) __attribute__((amdgpu_waves_per_eu(KM <= 1024 ? 8 : 6))) void k_topk_kl(const uint16_t *__restrict__ student,
-                                                 const uint16_t *__restrict__ teacher, int V,
-                                                 int K, const uint8_t *__restrict__ valid,
+                                                 const uint16_t *__restrict__ teacher, int T,
+                                                 int V, int K, const uint8_t *__restrict__ valid,
                                                  const float *__restrict__ inv_n,
                                                  int32_t *__restrict__ out_idx,
                                                  float *__restrict__ out_grad,
@@ -354,7 +354,8 @@ __global__ __launch_bounds__(kKT) __attribute__((amdgpu_waves_per_eu(KM <= 1024 
   __shared__ KLShared sh;
   __shared__ KLBig<KM> xs;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const size_t row = blockIdx.x;
+  const size_t row = block_of_grid();
+  if (row >= (size_t)T) return;
   const uint4 *trow = reinterpret_cast<const uint4 *>(teacher + row * (size_t)V);
   const uint32_t nvec = (uint32_t)V / 8u;
   int par = 0;
@@ -677,8 +678,8 @@ void launch_topk_kl(const uint16_t *student, const uint16_t *teacher, int T, int
   if (T > 0) {
     auto k = reverse ? (K <= 1024 ? k_topk_kl<true, 1024> : k_topk_kl<true, kTopKMax>)
                      : (K <= 1024 ? k_topk_kl<false, 1024> : k_topk_kl<false, kTopKMax>);
-    hipLaunchKernelGGL(k, dim3(T), dim3(kKT), 0, st, student, teacher, V, K, valid, inv_n, idx,
-                       grad, loss_tok);
+    hipLaunchKernelGGL(k, block_grid(T), dim3(kKT), 0, st, student, teacher, T, V, K, valid, inv_n,
+                       idx, grad, loss_tok);
   }
   hipLaunchKernelGGL(k_kl_mean, dim3(1), dim3(1024), 0, st, loss_tok, T, inv_n, loss_mean);
 }

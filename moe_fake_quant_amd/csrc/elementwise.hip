@@ -186,10 +186,12 @@ __global__ __launch_bounds__(kThreads) void k_observer_lanes(const bf16x8_t *__r
 // Groups longer than 64 vectors (per-channel scales): one block per group.
 template <int FMT>
 __global__ __launch_bounds__(kThreads) void k_observer_block(const bf16x8_t *__restrict__ w,
-                                                             int vec_per_group,
+                                                             int vec_per_group, uint32_t ngroups,
                                                              float *__restrict__ scale,
                                                              float *__restrict__ zero_point) {
-  const bf16x8_t *p = w + (size_t)blockIdx.x * vec_per_group;
+  const uint32_t group = block_of_grid();
+  if (group >= ngroups) return;
+  const bf16x8_t *p = w + (size_t)group * vec_per_group;
   float amax = 0.0f, mn = 0.0f, mx = 0.0f;
   for (int i = threadIdx.x; i < vec_per_group; i += blockDim.x) {
     float x[8];
@@ -219,13 +221,13 @@ __global__ __launch_bounds__(kThreads) void k_observer_block(const bf16x8_t *__r
     }
     if (FMT == FQ_FMT_INT8 || FMT == FQ_FMT_FP8_E4M3) {
       float s = amax / (FMT == FQ_FMT_INT8 ? 127.0f : kE4M3Max);
-      scale[blockIdx.x] = s == 0.0f ? 1.0f : s;
+      scale[group] = s == 0.0f ? 1.0f : s;
     } else {  // int4
       float s = (mx - mn) / 15.0f;
       s = s == 0.0f ? 1.0f : s;
       float r = 1.0f / s;
-      scale[blockIdx.x] = s;
-      zero_point[blockIdx.x] = fminf(fmaxf(rintf(-mn * r), 0.0f), 15.0f);
+      scale[group] = s;
+      zero_point[group] = fminf(fmaxf(rintf(-mn * r), 0.0f), 15.0f);
     }
   }
 }
@@ -673,7 +675,8 @@ void launch_observer_weight(const uint16_t *w, fq_shape s, int fmt, int group, f
   } else {
     uint32_t ngroups = nvec / vpg;
 #define FQ_OBB(F) \
-  hipLaunchKernelGGL(k_observer_block<F>, dim3(ngroups), dim3(kThreads), 0, st, wv, vpg, scale, zero_point)
+  hipLaunchKernelGGL(k_observer_block<F>, block_grid((int)ngroups), dim3(kThreads), 0, st, wv, vpg, ngroups, \
+                     scale, zero_point)
     switch (fmt) {
       case FQ_FMT_INT8: FQ_OBB(FQ_FMT_INT8); break;
       case FQ_FMT_INT4: FQ_OBB(FQ_FMT_INT4); break;

@@ -388,7 +388,7 @@ void launch_norm_fwd(const uint16_t *x, const uint16_t *b, const float *gate, fl
   a.scale = scale;
   with_row_form(H, [&](auto wpr, auto vpt) {
     constexpr int W = decltype(wpr)::value, V = decltype(vpt)::value;
-    hipLaunchKernelGGL((k_norm_fwd<W, V>), row_grid(ceil_div(T, kBlockRows<W>)), dim3(kRowThreads<W>), 0,
+    hipLaunchKernelGGL((k_norm_fwd<W, V>), block_grid(ceil_div(T, kBlockRows<W>)), dim3(kRowThreads<W>), 0,
                        st, a);
   });
 }
@@ -422,7 +422,7 @@ void launch_norm_bwd(const uint16_t *dy, const uint16_t *dn, const uint16_t *y, 
                          a);
     else
       // (the kernel strides over the rows: along x alone)
-      hipLaunchKernelGGL((k_norm_bwd<W, V, false>), dim3(row_grid(ceil_div(T, kBlockRows<W>)).x), threads, 0,
+      hipLaunchKernelGGL((k_norm_bwd<W, V, false>), dim3(block_grid(ceil_div(T, kBlockRows<W>)).x), threads, 0,
                          st, a);
   });
   if (dw)
@@ -435,10 +435,10 @@ void launch_quantize_tokens(const uint16_t *x, int rows, int K, const int32_t *n
   const bf16x8_t *v = reinterpret_cast<const bf16x8_t *>(x);
   uint2 *c = reinterpret_cast<uint2 *>(codes);
   if (K <= 1024)
-    hipLaunchKernelGGL((k_quantize_tokens<1, 2>), row_grid(ceil_div(rows, 4)), dim3(256), 0, st, v, rows,
+    hipLaunchKernelGGL((k_quantize_tokens<1, 2>), block_grid(ceil_div(rows, 4)), dim3(256), 0, st, v, rows,
                        K / 8, n_rows, c, scale);
   else
-    hipLaunchKernelGGL((k_quantize_tokens<4, 4>), row_grid(rows), dim3(256), 0, st, v, rows, K / 8, n_rows,
+    hipLaunchKernelGGL((k_quantize_tokens<4, 4>), block_grid(rows), dim3(256), 0, st, v, rows, K / 8, n_rows,
                        c, scale);
 }
 

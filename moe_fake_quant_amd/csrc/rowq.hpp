@@ -14,17 +14,10 @@ constexpr int kRowThreads = WPR == 1 ? 256 : WPR * 64;
 template <int WPR>
 constexpr int kBlockRows = WPR == 1 ? 4 : 1;
 
-// One block a kBlockRows rows. A grid of 2^32 or more threads along x loses blocks without an
-// error, and short rows reach that (2^26 of one wave each): blocks beyond 2^22 go along y.
-inline dim3 row_grid(int blocks) {
-  constexpr int kX = 1 << 22;
-  return blocks <= kX ? dim3(blocks) : dim3(kX, ceil_div(blocks, kX));
-}
 // the row of this thread's group; the grid's last blocks may lie behind the last row
 template <int WPR>
 __device__ __forceinline__ uint32_t grid_row() {
-  return (blockIdx.y * gridDim.x + blockIdx.x) * (uint32_t)kBlockRows<WPR> +
-         threadIdx.x / (uint32_t)(WPR * 64);
+  return block_of_grid() * (uint32_t)kBlockRows<WPR> + threadIdx.x / (uint32_t)(WPR * 64);
 }
 
 // Sums of N values over the row's lanes, the same in each of them and in a fixed

@@ -1,5 +1,5 @@
-"""Row counts whose blocks pass 2^32 threads: the token codes and the norms over a repeated
-pattern of rows, every row with the bits of a small call."""
+"""Row counts whose blocks pass 2^32 threads: token codes, norms, distillation and observed
+groups over a repeated pattern of rows, every row with the bits of a small call."""
 import pytest
 import torch
 
@@ -63,3 +63,43 @@ def test_norms_of_many_rows(T, H):
     F.fq_norm_residual_bwd(None, n1, p, None, None, 1.0, None, w, EPS, P, H, dx=d1)
     F.fq_norm_residual_bwd(None, n, x, None, None, 1.0, None, w, EPS, T, H, dx=n)
     repeats(n, d1)
+
+
+def test_distillation_of_many_rows():
+    """2^23 rows of 512 threads each."""
+    T, V, K = (1 << 23) + 3 * P, 16, 3
+    print(f"[many rows] top-K KL {T}x{V}", flush=True)
+    (ps, s), (pt, t) = pattern(V, 3, T), pattern(V, 4, T)
+    e = lambda *d, t=torch.float32: torch.empty(*d, dtype=t, device="cuda")  # noqa: E731
+    ws = e(256, t=torch.uint8)
+
+    def run(s, t, n):
+        idx, grad, tok, mean = e(n, K, t=torch.int32), e(n, K), e(n), e(1)
+        F.fq_topk_kl(s, t, n, V, K, False, None, idx, grad, tok, mean, ws)
+        return idx, grad, tok, float(mean)
+
+    (i1, g1, l1, m1), (idx, grad, tok, mean) = run(ps, pt, P), run(s, t, T)
+    repeats(idx, i1)
+    repeats(tok, l1)
+    repeats(grad, grad[:P])
+    # one division by the number of rows apart
+    assert torch.allclose(grad[:P] * T, g1 * P, rtol=2.0 ** -21, atol=0)
+    # T is not a whole number of patterns: the mean of its rows, within 2^-11 of their sum of
+    # magnitudes (2^13 terms a thread, then a tree)
+    whole, rest = divmod(T, P)
+    want = float((l1.double().sum() * whole + l1[:rest].double().sum()) / T)
+    assert abs(mean - want) <= 2.0 ** -10 * float(l1.abs().mean())
+
+
+def test_observed_groups_of_many_rows():
+    """2^24 groups of 48 elements, a block of 256 threads each."""
+    N, K = (1 << 24) + 3 * P, 48
+    print(f"[many rows] observer {N}x{K}", flush=True)
+    p, w = pattern(K, 5, N)
+    s, s1, z, z1 = (torch.empty(n, device="cuda") for n in (N, P, N, P))
+    for fmt in (F.FMT_INT8, F.FMT_INT4):
+        zz = (z, z1) if fmt == F.FMT_INT4 else (None, None)
+        F.observer_absmax_init(p, (1, P, K), fmt, K, 0, s1, zz[1])
+        F.observer_absmax_init(w, (1, N, K), fmt, K, 0, s, zz[0])
+        repeats(s, s1)
+    repeats(z, z1)
