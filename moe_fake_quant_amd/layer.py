@@ -468,8 +468,8 @@ class MoEFakeQuantLayer:
                      probs: torch.Tensor) -> torch.Tensor:
         """The layer over the exported int8 stacks for up to T_max tokens: the tokens and
         the SwiGLU rows as int8 codes with a scale each, both products on the codes. The
-        result is the layer's own buffer, overwritten by the next call; nothing that a
-        backward needs is touched."""
+        result is the layer's own buffer, overwritten by the next call; calls of one layer
+        share their buffers and must not overlap. Nothing that a backward needs is touched."""
         self._check_int8()
         T = x.shape[0]
         if x.shape != (T, self.H) or x.dtype != torch.bfloat16:
